@@ -35,3 +35,11 @@ from .binding import (  # noqa: F401
     SCHEDULE_ONE_LAUNCH,
     SCHEDULE_AUX_STREAM,
 )
+from .kv import (  # noqa: F401
+    KVCache,
+    dflash_kv_write,
+    dflash_kv_read,
+    dflash_kv_commit,
+    dflash_tree_attention,
+    tree_attention_workspace_size,
+)

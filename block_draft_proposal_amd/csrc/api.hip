@@ -7,12 +7,15 @@
 #include <cstdio>
 #include <string>
 
+#include "api_common.h"
 #include "dflash.h"
 #include "dflash_internal.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace dflash {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -29,20 +32,23 @@ int ok() {
   return DFLASH_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-int elem_bytes(int32_t dtype) { return dtype == DFLASH_BF16 ? 2 : 4; }
-bool dtype_ok(int32_t dtype) { return dtype == DFLASH_F32 || dtype == DFLASH_BF16; }
-hipStream_t as_hip(dflash_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
-
 int launch_status(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(DFLASH_ERR_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
   return DFLASH_OK;
 }
 
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
+}  // namespace dflash
+
+namespace {
+
+using dflash::aligned16;
+using dflash::as_hip;
+using dflash::dtype_ok;
+using dflash::elem_bytes;
+using dflash::fail;
+using dflash::launch_status;
+using dflash::ok;
+using dflash::overlaps;
 
 constexpr size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 constexpr int64_t kMaxVocab = (int64_t)1 << 24;
