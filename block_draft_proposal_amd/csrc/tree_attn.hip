@@ -1,7 +1,7 @@
 // Attention of drafted nodes over a paged cache.
 //
-// One request and kv head form M = nodes * group query rows over the same
-// keys.  A workgroup takes MT = 32 RW of them and walks KT keys a step:
+// One request and kv head form n * group query rows over the same keys.  A
+// workgroup takes kRows = 32 RW of them (an item) and walks kKeys keys a step:
 //
 //   S^T = K Q^T        v_mfma_f32_32x32x16_bf16, a lane holds 16 scores of one row
 //   running maximum, p = 2^(s - m), running sum          in registers
@@ -16,14 +16,18 @@
 // and become bf16 (exactly) on the way into the product; their scales, powers
 // of two, multiply the scores and the weights.
 //
-// W = RW KW waves: RW share the rows, KW the keys of a step (few rows leave
-// waves to spare; they join their sums at the end).
+// A workgroup's waves are RW (rows) x KW (keys of a step): few rows leave
+// waves to spare, which split the keys and join their sums at the end.
 //
-// Work is split evenly whatever the lengths: the steps of all (request, kv
-// head, row tile) items form one line that is cut into equal pieces, one for
-// each workgroup.  A piece that covers an item writes its result; pieces of a
-// cut item leave (m, l, O) in the workspace, at most two to a workgroup, and a
-// second kernel joins them in a fixed order.
+// Work is split evenly whatever the lengths: the steps of all items, with a
+// constant for what an item costs besides, form one line that is cut into
+// equal pieces, one for each workgroup.  A piece that covers an item writes
+// its result; pieces of a cut item leave (m, l, O) in the workspace, at most
+// two to a workgroup, and a second kernel joins them in a fixed order.
+//
+// Loads run two steps ahead of the products and do not stop at an item's end:
+// each step's rows are looked up (page table, then addresses into LDS) by one
+// thread a row, two steps before its direct loads are issued.
 #include "kv_cache.h"
 
 namespace dflash {
@@ -40,7 +44,7 @@ struct Shape {
   static constexpr int kKeyWaves = kRowBytes == 512 ? (RW == 1 ? 2 : 1) : 4 / RW;
   static constexpr int kKeys = kRowBytes == 512 ? (RW == 1 ? 64 : 32)      // keys of a step
                                : RW == 1        ? 128
-                               : RW == 2        ? (kRowBytes == 256 ? 64 : 128)
+                               : RW == 2        ? (DT == DFLASH_BF16 && D == 128 ? 64 : 128)
                                                 : 64;
   static constexpr int kRows = 32 * RW;
   static constexpr int kWaves = RW * kKeyWaves, kThreads = 64 * kWaves;
@@ -48,17 +52,17 @@ struct Shape {
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kTile = kKeys * kRowBytes;                          // bytes of K (or V) in a step
   static constexpr int kLoads = kTile / 1024 / kWaves;                     // direct loads of K (or V) per thread
-  static constexpr int kPages = 1024;                                      // page ids held in LDS
-  static constexpr int kIdsAt = 4 * kTile;
-  static constexpr int kScalesAt = kIdsAt + 4 * kPages;                    // [2 stages][K, V][kKeys] fp32
-  static constexpr int kStatsAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 16 * kKeys);   // [kKeyWaves][kRows] m, l
+  static constexpr int kRowsAt = 4 * kTile;                                // [2 stages][kKeys] byte offsets, int64
+  static constexpr int kScalesAt = kRowsAt + 16 * kKeys;                   // [2 stages][K, V][kKeys] fp32
+  static constexpr int kBadAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 16 * kKeys);   // [4 steps][2] a row without a page
+  static constexpr int kStatsAt = kBadAt + 32;                             // [kKeyWaves][kRows] m, l
   static constexpr int kLds = kStatsAt + 8 * kKeyWaves * kRows;
   static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;                 // workgroups of a CU
   static constexpr int kPartOdd = kRows * (D + 2);                         // a partial: O [kRows][D], m and l of each
   static constexpr int kPartFloats = kPartOdd + 4;                         // row, whether odd values were left out
   static_assert(kSubs >= 1 && kLoads >= 1 && kTile % (1024 * kWaves) == 0, "a step splits over the waves");
-  static_assert((kKeyWaves - 1) * kRows * D * 4 <= 4 * kTile, "the join fits where the stages were");
-  static_assert(DT == DFLASH_BF16 || 2 * kKeys <= kThreads, "one scale per thread");
+  static_assert(kKeyWaves / 2 * kRows * D * 4 <= 2 * kTile, "the join fits where one stage was");
+  static_assert(kKeys <= kThreads && kKeys <= 128, "one thread looks up a row");
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
 
   // Chunk c of stage row r lies in slot c ^ swizzle(r).  8 lanes of a 16-byte
@@ -70,6 +74,14 @@ struct Shape {
     else return kRowBytes == 256 ? r & 15 : kRowBytes == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
   }
 };
+
+// What an item costs besides its steps, in steps: the first step's latency,
+// the join of the key waves and the output.
+constexpr int kItemCost = 2;
+// A piece is at least this long: below, the join costs more than the split saves.
+constexpr int kMinPiece = 4;
+// Lengths beyond this have no positions (their rows are NaN).
+constexpr int kMaxLen = 0x7fffffff - (1 << 17);
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -178,104 +190,207 @@ __device__ __forceinline__ bool odd_values(u32x4& w) {
   return any;
 }
 
-// A request's share of the line of steps.
+// Uniform loads of a batch's arrays, which no kernel here writes: through the
+// constant address space they are scalar loads, which do not wait for (or
+// make anything wait for) the vector loads in flight.
+__device__ __forceinline__ int32_t uniform_load(const int32_t* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[i];
+}
+
+// A request's share of the line.
 struct Req {
   int32_t first;             // its first row
   int32_t n;                 // nodes
-  int64_t start;             // prefix positions
-  int64_t len;               // start + n
-  int32_t steps;             // ceil(len / keys)
+  int32_t start;             // prefix positions
+  int32_t len;               // start + n, at most kMaxLen
+  int32_t steps;             // ceil(len / keys); 0 without nodes
   int32_t tiles;             // row tiles
+  bool over;                 // start + n is beyond kMaxLen
+  __device__ __forceinline__ int64_t cost(int heads) const {
+    return steps ? (int64_t)(steps + kItemCost) * (tiles * heads) : 0;
+  }
 };
-__device__ __forceinline__ Req request(const TreeArgs& a, int r, int keys, int rows, int group) {
+template <int KEYS, int ROWS>
+__device__ __forceinline__ Req make_request(const TreeArgs& a, int32_t first, int32_t end, int32_t start, int group) {
   Req q;
-  const int64_t first = a.c.offsets[r], end = min((int64_t)a.c.offsets[r + 1], a.c.n_rows);
-  const int64_t n = first < 0 ? 0 : max((int64_t)0, min(end - first, (int64_t)a.max_nodes));
-  q.first = (int32_t)first;
+  const int64_t n = first < 0 ? 0 : max((int64_t)0, min(min((int64_t)end, a.c.n_rows) - first, (int64_t)a.max_nodes));
+  q.first = first;
   q.n = (int32_t)n;
-  q.start = max(a.c.start[r], 0);
-  q.len = q.start + n;
-  q.steps = n > 0 ? (int32_t)((q.len + keys - 1) / keys) : 0;
-  q.tiles = (int32_t)((n * group + rows - 1) / rows);
+  q.start = max(start, 0);
+  q.over = q.start + n > kMaxLen;
+  q.len = (int32_t)min(q.start + n, (int64_t)kMaxLen);
+  q.steps = n > 0 ? (q.len + KEYS - 1) / KEYS : 0;
+  q.tiles = (q.n * group + ROWS - 1) / ROWS;
   return q;
 }
 
-// The line of steps: its length, this workgroup's piece [u0, u1), and the
-// request that holds u0 with the steps before it.
+// The line and this workgroup's piece [u0, u1) of it; req and before: the
+// request that u0 lies in and the line before it.
 struct Piece {
   int64_t total, u0, u1, before;
   int32_t pieces, w, req;
   __device__ __forceinline__ int64_t begin(int64_t i) const { return total * i / pieces; }
-  // the piece that step u lies in
+  // the piece that point u lies in
   __device__ __forceinline__ int32_t of(int64_t u) const { return (int32_t)(((u + 1) * pieces - 1) / total); }
 };
 
-template <int THREADS>
-__device__ __forceinline__ Piece find_piece(const TreeArgs& a, int keys, int rows, int group) {
-  constexpr int kWaves = THREADS / 64;
-  __shared__ int64_t sums[kWaves];
+// x of the lanes that a DPP control names, 0 where there is none.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int64_t dpp_i64(int64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, ROW_MASK, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), CTRL, ROW_MASK, 0xf, false);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+// Inclusive sums along a wave.
+__device__ __forceinline__ int64_t wave_scan(int64_t x) {
+  x += dpp_i64<0x111, 0xf>(x);                    // row_shr 1, 2, 4, 8
+  x += dpp_i64<0x112, 0xf>(x);
+  x += dpp_i64<0x114, 0xf>(x);
+  x += dpp_i64<0x118, 0xf>(x);
+  x += dpp_i64<0x142, 0xa>(x);                    // row_bcast 15, then 31
+  x += dpp_i64<0x143, 0xc>(x);
+  return x;
+}
+
+// x of the first lane, known to be the same in all: kept in scalar registers.
+__device__ __forceinline__ int64_t uniform_i64(int64_t x) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int32_t)(x >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int32_t)x);
+}
+
+template <class S>
+__device__ __forceinline__ Piece find_piece(const TreeArgs& a, int group) {
+  __shared__ int64_t sums[S::kWaves];
   __shared__ int64_t found[2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n_req = a.c.n_req;
-  auto steps_of = [&](int r) -> int64_t {
+  const int tid = threadIdx.x, wave = tid >> 6, n_req = a.c.n_req;
+  auto cost_of = [&](int r) -> int64_t {
     if (r >= n_req) return 0;
-    const Req q = request(a, r, keys, rows, group);
-    return (int64_t)q.steps * q.tiles * a.c.n_kv_heads;
+    return make_request<S::kKeys, S::kRows>(a, a.c.offsets[r], a.c.offsets[r + 1], a.c.start[r], group).cost(a.c.n_kv_heads);
   };
-  const int64_t mine = steps_of(tid);
-  int64_t sum = mine;
-  for (int r = tid + THREADS; r < n_req; r += THREADS) sum += steps_of(r);
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) sums[wave] = sum;
-  __syncthreads();
+  // the first kThreads requests' sums stay in registers; more come in rounds
+  const int64_t own0 = cost_of(tid), scan0 = wave_scan(own0);
   Piece p;
   p.total = 0;
-  for (int i = 0; i < kWaves; ++i) p.total += sums[i];
-  __syncthreads();
-  p.pieces = (int32_t)min((int64_t)gridDim.x, p.total);
-  p.w = (int)blockIdx.x < p.pieces ? (int)xcd_contiguous(blockIdx.x, p.pieces) : p.pieces;
-  p.u0 = p.u1 = 0;
+  for (int r0 = 0; r0 < n_req; r0 += S::kThreads) {
+    const int64_t scan = r0 == 0 ? scan0 : wave_scan(cost_of(r0 + tid));
+    if (r0) __syncthreads();
+    if ((tid & 63) == 63) sums[wave] = scan;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < S::kWaves; ++i) p.total += sums[i];
+  }
+  p.total = uniform_i64(p.total);
+  p.pieces = (int32_t)min((int64_t)gridDim.x, (p.total + kMinPiece - 1) / kMinPiece);
+  p.w = (int)blockIdx.x < p.pieces ? (int)xcd_contiguous(blockIdx.x, p.pieces) : (int)blockIdx.x;
+  p.u0 = p.u1 = p.before = 0;
   p.req = n_req;
-  p.before = 0;
   if (p.w >= p.pieces) return p;                  // the whole workgroup: nothing to do
   p.u0 = p.begin(p.w);
   p.u1 = p.begin(p.w + 1);
   int64_t run = 0;
-  for (int r0 = 0; r0 < n_req; r0 += THREADS) {
-    int64_t x = r0 == 0 ? mine : steps_of(r0 + tid);
-    const int64_t own = x;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t y = __shfl_up(x, o, 64);
-      if (lane >= o) x += y;
+  for (int r0 = 0; r0 < n_req && uniform_i64(run) <= p.u0; r0 += S::kThreads) {
+    int64_t own = own0, scan = scan0;
+    if (n_req > S::kThreads) {                    // sums holds the last round's
+      if (r0) {
+        own = cost_of(r0 + tid);
+        scan = wave_scan(own);
+      }
+      __syncthreads();
+      if ((tid & 63) == 63) sums[wave] = scan;
+      __syncthreads();
     }
-    if (lane == 63) sums[wave] = x;
-    __syncthreads();
-    int64_t ahead = run, all = 0;
-    for (int i = 0; i < kWaves; ++i) {
-      if (i < wave) ahead += sums[i];
+    int64_t all = 0;
+    scan += run;
+#pragma unroll
+    for (int i = 0; i < S::kWaves; ++i) {
+      if (i < wave) scan += sums[i];
       all += sums[i];
     }
-    x += ahead;                                   // steps up to and with request r0 + tid
-    if (x - own <= p.u0 && p.u0 < x) {
+    if (scan - own <= p.u0 && p.u0 < scan) {
       found[0] = r0 + tid;
-      found[1] = x - own;
+      found[1] = scan - own;
     }
     run += all;
-    __syncthreads();
-    if (run > p.u0) break;
   }
-  p.req = (int32_t)found[0];
-  p.before = found[1];
   __syncthreads();
+  p.req = __builtin_amdgcn_readfirstlane((int32_t)found[0]);
+  p.before = uniform_i64(found[1]);
   return p;
 }
 
+// Walks the steps of a piece.
+template <class S>
+struct Cursor {
+  Req q;
+  int64_t at;                // where the item begins on the line
+  int64_t u0, u1;
+  int32_t req, item, head, tile, t, t1;
+  bool valid;
+
+  // The item's steps that lie in the piece; on to the next item where there are none.
+  __device__ __forceinline__ void settle(const TreeArgs& a, int group) {
+    for (;;) {
+      if (at >= u1) {
+        valid = false;
+        return;
+      }
+      if (item >= q.tiles * a.c.n_kv_heads || q.steps == 0) {
+        if (++req >= a.c.n_req) {
+          valid = false;
+          return;
+        }
+        load(a, group);
+        item = 0;
+        continue;
+      }
+      const int64_t lo = u0 - at - kItemCost, hi = u1 - at - kItemCost;
+      t = (int32_t)max(lo, (int64_t)0);
+      t1 = (int32_t)min(hi, (int64_t)q.steps);
+      if (t < t1) {
+        head = item / q.tiles;
+        tile = item - head * q.tiles;
+        return;
+      }
+      at += q.steps + kItemCost;
+      ++item;
+    }
+  }
+  __device__ __forceinline__ void load(const TreeArgs& a, int group) {
+    q = make_request<S::kKeys, S::kRows>(a, uniform_load(a.c.offsets, req), uniform_load(a.c.offsets, req + 1),
+                                         uniform_load(a.c.start, req), group);
+  }
+  __device__ __forceinline__ void begin(const TreeArgs& a, const Piece& p, int group) {
+    u0 = p.u0;
+    u1 = p.u1;
+    req = p.req;
+    load(a, group);
+    const int32_t per_item = q.steps + kItemCost;
+    item = (int32_t)((p.u0 - p.before) / per_item);
+    at = p.before + (int64_t)item * per_item;
+    valid = true;
+    settle(a, group);
+  }
+  __device__ __forceinline__ void next_item(const TreeArgs& a, int group) {
+    at += q.steps + kItemCost;
+    ++item;
+    settle(a, group);
+  }
+};
+
+// What the join needs of a cut item (n: its pieces; 0: none).
+struct JoinItem {
+  int32_t piece, n, rows;           // first piece (the item in its slot 1, in later ones' slot 0)
+  int32_t first, nodes, start, req, head, tile;
+  int32_t pad[3];
+};
+
 // Whether a node sees anything: a prefix, or a bit of its mask.
-__device__ __forceinline__ bool sees_any(const TreeArgs& a, const Req& q, int node) {
-  if (q.start > 0 || !a.mask) return true;
-  const uint64_t* m = a.mask + (int64_t)(q.first + node) * a.mask_words;
+__device__ __forceinline__ bool sees_any(const TreeArgs& a, int32_t first, int32_t n, int32_t start, int node) {
+  if (start > 0 || !a.mask) return true;
+  const uint64_t* m = a.mask + (int64_t)(first + node) * a.mask_words;
   uint64_t any = 0;
-  for (int w = 0; w * 64 < q.n; ++w) {
-    const int left = q.n - w * 64;
+  for (int w = 0; w * 64 < n; ++w) {
+    const int left = n - w * 64;
     any |= m[w] & (left >= 64 ? ~0ull : (1ull << left) - 1);
   }
   return any != 0;
@@ -285,15 +400,15 @@ __device__ __forceinline__ bool sees_any(const TreeArgs& a, const Req& q, int no
 // that are not finite (a sum with such a value is that value, and of both
 // infinities NaN, whatever the weights).
 template <int DT, int D>
-__device__ __forceinline__ void add_odd(const TreeArgs& a, const Req& q, int req, int head, int node, int d,
-                                                  float (&f)[4]) {
+__device__ __forceinline__ void add_odd(const TreeArgs& a, int32_t first, int32_t n, int32_t start, int req, int head,
+                                        int node, int d, float (&f)[4]) {
   constexpr int kSize = DT == DFLASH_BF16 ? 2 : 1;
 #pragma unroll 1
-  for (int j = 0; j < q.n; ++j) {
-    if (a.mask ? !((a.mask[(int64_t)(q.first + node) * a.mask_words + (j >> 6)] >> (j & 63)) & 1) : j > node) continue;
+  for (int j = 0; j < n; ++j) {
+    if (a.mask ? !((a.mask[(int64_t)(first + node) * a.mask_words + (j >> 6)] >> (j & 63)) & 1) : j > node) continue;
     int64_t page;
     int32_t slot;
-    if (!kv_locate(a.c, a.c.table + req * a.c.table_stride, q.start + j, page, slot)) continue;
+    if (!kv_locate(a.c, a.c.table + req * a.c.table_stride, (int64_t)start + j, page, slot)) continue;
     const unsigned char* v = a.c.v + page * a.c.page_bytes + ((int64_t)(head * a.c.page_size + slot) * D + d) * kSize;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -312,17 +427,21 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   constexpr int kRB = S::kRowBytes, kKeys = S::kKeys, kBlocks = D / 32, kSteps16 = D / 16;
   constexpr int kPerBlock = DT == DFLASH_BF16 ? 4 : 2;   // chunks of a 32-column block
   extern __shared__ __align__(16) unsigned char ta_smem[];
-  int32_t* ids = reinterpret_cast<int32_t*>(ta_smem + S::kIdsAt);
+  int64_t* row_at = reinterpret_cast<int64_t*>(ta_smem + S::kRowsAt);
   float* scales = reinterpret_cast<float*>(ta_smem + S::kScalesAt);
-  float* stats = reinterpret_cast<float*>(ta_smem + S::kStatsAt);
+  int32_t* bad_pages = reinterpret_cast<int32_t*>(ta_smem + S::kBadAt);
+  float2* stats = reinterpret_cast<float2*>(ta_smem + S::kStatsAt);
   const KvView& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rw = wave % RW, kw = wave / RW, half = lane >> 5, l32 = lane & 31;
   const int group = per_group.d;
-  const Piece piece = find_piece<S::kThreads>(a, kKeys, S::kRows, group);
+  const Piece piece = find_piece<S>(a, group);
+  JoinItem* joins = static_cast<JoinItem*>(a.workspace);
+  if (tid == 0) joins[piece.w * 2].n = joins[piece.w * 2 + 1].n = 0;
   if (piece.w >= piece.pieces) return;
-  // log2(e) and the softmax scale; 8-bit caches carry it in K's scales
-  const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_BF16 ? c2 : 1.f;
+  float* parts = reinterpret_cast<float*>(joins + 2 * gridDim.x) + (int64_t)piece.w * 2 * S::kPartFloats;
+  // log2(e) and the softmax scale; an int8 cache carries it in K's scales
+  const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_I8 ? 1.f : c2;
 
   // K reads: row l32 of a 32-key block, chunk 2t + half in slot (2t) ^ kx
   const int kx = half ^ S::swizzle(l32);
@@ -333,134 +452,119 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   const int vr = DT == DFLASH_BF16 ? 4 * half + vj : 8 * (vj >> 2) + 4 * half + (vj & 3);
   const int vx = (DT == DFLASH_BF16 ? 2 * (g16 & 1) + ((i16 >> 1) & 1) : g16 & 1) ^ S::swizzle(vr);
   const int vbase = vr * kRB + (i16 & 1) * 8;
+  // direct loads: lane's row of a 1 KB block, and its chunk's place in the row
+  // (the swizzle of a row repeats from block to block of a wave or is taken per load)
+  const int lrow = lane / S::kChunks, lslot = lane % S::kChunks;
 
-  int req = piece.req;
-  int64_t req_begin = piece.before, u = piece.u0;
-  while (u < piece.u1) {
-    const Req q = request(a, req, kKeys, S::kRows, group);
-    const int64_t req_units = (int64_t)q.steps * q.tiles * c.n_kv_heads;
-    if (u >= req_begin + req_units) {              // also requests without nodes
-      req_begin += req_units;
-      ++req;
-      continue;
-    }
-    const int32_t item = (int32_t)((u - req_begin) / q.steps), t0 = (int32_t)((u - req_begin) - (int64_t)item * q.steps);
-    const int32_t t1 = (int32_t)min((int64_t)q.steps, t0 + (piece.u1 - u));
-    const int head = item / q.tiles, tile = item - head * q.tiles;
-    const int rows = min(S::kRows, q.n * group - tile * S::kRows);   // rows of this tile
-    const bool whole = t0 == 0 && t1 == q.steps, first_item = u == piece.u0;
-    const int row = rw * 32 + l32;                 // this lane's row of the tile, and its node and head
-    const int flat = tile * S::kRows + min(row, rows - 1), node = per_group.div(flat), gh = flat - node * group;
-    const int32_t* table = c.table + req * c.table_stride;
+  // The step being looked up, two or three ahead of the products.
+  Cursor<S> feed;
+  feed.begin(a, piece, group);
+  Cursor<S> w = feed;                              // the step of the products
+  const bool feeder = tid < kKeys;                 // this thread looks up row tid of each step
+  int32_t page_id = 0, row_in_page = 0;            // of the next step to get addresses
+  uint32_t k_byte = 0, v_byte = 0;                 // scale bytes of the step after
 
-    // this row's query, in the order K's chunks have in the product
-    bf16x8_t qf[kSteps16];
-    {
-      const uint16_t* qp = a.q + (int64_t)(q.first + node) * a.q_row + (int64_t)(head * group + gh) * a.q_head;
+  bf16x8_t qf[kSteps16];                           // this row's query, in the order K's chunks have in the product
+  int row = rw * 32 + l32, rows = 0, node = 0, gh = 0;   // this lane's row of the item, its node and head of the group
+  auto load_query = [&]() {
+    rows = min(S::kRows, w.q.n * group - w.tile * S::kRows);
+    const int flat = w.tile * S::kRows + min(row, rows - 1);
+    node = per_group.div(flat);
+    gh = flat - node * group;
+    const uint16_t* qp = a.q + (int64_t)(w.q.first + node) * a.q_row + (int64_t)(w.head * group + gh) * a.q_head;
 #pragma unroll
-      for (int t = 0; t < kSteps16; ++t) {
-        const int d = DT == DFLASH_BF16 ? 16 * t + 8 * half : 32 * (t / 2) + 16 * half + 8 * (t & 1);
-        qf[t] = __builtin_bit_cast(bf16x8_t, ld16(qp + d));
-      }
+    for (int t = 0; t < kSteps16; ++t) {
+      const int d = DT == DFLASH_BF16 ? 16 * t + 8 * half : 32 * (t / 2) + 16 * half + 8 * (t & 1);
+      qf[t] = __builtin_bit_cast(bf16x8_t, ld16(qp + d));
     }
+  };
 
-    // page ids in LDS, a window of them at a time
-    const int last_page = c.per_page.div((int)min(q.len - 1, (int64_t)0x7fffffff));
-    int page0 = 0, page_end = 0;
-    bool bad = q.len > 0x7fffffff;
-    auto load_pages = [&](int from) {
-      step_barrier();
-      page0 = from;
-      page_end = min(from + S::kPages, last_page + 1);
-      for (int i = from + tid; i < page_end; i += S::kThreads) {
-        int id = i < c.table_width ? table[i] : -1;
-        if (id < 0 || id >= c.n_pages) {
-          bad = true;
-          id = 0;
-        }
-        ids[i - from] = id;
-      }
-      step_barrier();
-    };
-    // page id and row within its head's rows of position pos (at most the
-    // last held one: later rows of a step repeat it and are masked)
-    auto locate = [&](int64_t pos, int32_t& id, int32_t& r) {
-      const int p = (int)min(pos, min(q.len - 1, (int64_t)0x7fffffff)), idx = c.per_page.div(p);
-      id = ids[idx - page0];
-      r = head * c.page_size + (p - idx * c.page_size);
-    };
-    uint32_t scale_next = 0;                       // this thread's scale byte of the step issued last
-    auto issue = [&](int t) {
-      const int64_t p0 = (int64_t)t * kKeys;
-      const int need = c.per_page.div((int)min(min(p0 + kKeys, q.len) - 1, (int64_t)0x7fffffff));
-      if (need >= page_end) load_pages(c.per_page.div((int)min(p0, (int64_t)0x7fffffff)));
-      unsigned char* stage = ta_smem + (t & 1) * 2 * S::kTile;
-      if constexpr (DT != DFLASH_BF16) {
-        if (tid < 2 * kKeys) {
-          int32_t id, r;
-          locate(p0 + tid % kKeys, id, r);
-          scale_next = (tid < kKeys ? c.k_scale : c.v_scale)[id * c.scale_page_bytes + r];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < S::kLoads; ++i) {
-        const int blk = i * S::kWaves + wave, r = blk * (1024 / kRB) + lane / S::kChunks;
-        int32_t id, at;
-        locate(p0 + r, id, at);
-        const int64_t off = id * c.page_bytes + (int64_t)at * kRB + (((lane % S::kChunks) ^ S::swizzle(r)) << 4);
-        __builtin_amdgcn_global_load_lds((const void*)(c.k + off), (lds_void_t*)(stage + blk * 1024), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((const void*)(c.v + off), (lds_void_t*)(stage + S::kTile + blk * 1024), 16, 0, 0);
-      }
-    };
+  // Starts the look-up of the next step's pages; false after the last.
+  auto look_up = [&]() -> bool {
+    if (!feed.valid) return false;
+    if (feeder) {
+      // rows past the end repeat the last position; they are masked
+      const int pos = min(feed.t * kKeys + tid, feed.q.len - 1), idx = c.per_page.div(pos);
+      row_in_page = feed.head * c.page_size + (pos - idx * c.page_size);
+      page_id = -1;
+      if (idx < c.table_width) page_id = c.table[feed.req * c.table_stride + idx];
+    }
+    if (++feed.t == feed.t1) feed.next_item(a, group);
+    return true;
+  };
 
-    bool odd = false;                              // a node's value was not finite
-    f32x16_t o[kBlocks];
+  f32x16_t o[kBlocks];
+  float m, l;                                      // of this lane's row; l over this lane's keys only
+  bool bad, odd;                                   // a position without a page; a node's value that is not finite
+  int t_first;                                     // the item's first step here
+  auto clear = [&]() {
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
-    float m = -INFINITY, l = 0.f;                  // of this lane's row; l over this lane's keys only
+    m = -INFINITY;
+    l = 0.f;
+    bad = w.q.over;
+    odd = false;
+    t_first = w.t;
+  };
+  if (!w.valid) return;                            // the whole workgroup: its piece has no steps
+  load_query();
+  clear();
 
-    step_barrier();                                // the LDS is free of the previous item
-    issue(t0);
-    // the queries have arrived before the loop: no wait in it may be for them
-#pragma unroll
-    for (int i = 0; i < kSteps16; ++i) {
-      u32x4 w = __builtin_bit_cast(u32x4, qf[i]);
-      asm volatile("" : "+v"(w));
-      qf[i] = __builtin_bit_cast(bf16x8_t, w);
-    }
-    uint32_t scale_now = scale_next;
-    if (t0 + 1 < t1) issue(t0 + 1);
-    for (int t = t0; t < t1; ++t) {
-      if (t + 1 < t1) wait_vm<2 * S::kLoads>();
-      else wait_vm<0>();
+  // e0, e1, e2: whether steps g, g+1, g+2 exist.  Iteration g multiplies step
+  // g, writes step g+1's scales, gives step g+2 its addresses and its direct
+  // loads, and looks up step g+3's pages; the first two only fill.
+  bool e0 = false, e1 = false, e2 = look_up();
+  wait_vm<0>();
+  for (int s4 = 2;; s4 = (s4 + 1) & 3) {           // the iteration's step, modulo 4
+    const int g = s4 & 1;                          // its stage
+    wait_vm<2 * S::kLoads>();                      // all but step g+1's direct loads have arrived
+    step_barrier();
+    unsigned char* stage = ta_smem + g * 2 * S::kTile;
+    if (feeder) {
       if constexpr (DT != DFLASH_BF16) {
-        if (tid < 2 * kKeys)
-          scales[(t & 1) * 2 * kKeys + tid] = tid < kKeys ? kv_scale_value(scale_now) * c2 : kv_scale_value(scale_now);
+        float* sc = scales + (g ^ 1) * 2 * kKeys + tid;
+        sc[0] = DT == DFLASH_I8 ? kv_scale_value(k_byte) * c2 : kv_scale_value(k_byte);
+        sc[kKeys] = kv_scale_value(v_byte);
       }
-      step_barrier();
-      const unsigned char* ks = ta_smem + (t & 1) * 2 * S::kTile;
-      const unsigned char* vs = ks + S::kTile;
-      const int64_t p0 = (int64_t)t * kKeys;
-      const bool masked = p0 + kKeys > q.start;     // the step reaches the tree (or the end)
+      const bool no_page = page_id < 0 || page_id >= c.n_pages, use = e2 && !no_page;
+      const int64_t id = use ? page_id : 0;
+      const int32_t at = use ? row_in_page : 0;
+      row_at[g * kKeys + tid] = id * c.page_bytes + (int64_t)at * kRB;
+      const uint64_t any = __ballot(no_page);
+      if (lane == 0) bad_pages[((s4 + 2) & 3) * 2 + wave] = any != 0;
+      if constexpr (DT != DFLASH_BF16) {
+        k_byte = c.k_scale[id * c.scale_page_bytes + at];
+        v_byte = c.v_scale[id * c.scale_page_bytes + at];
+      }
+    }
+    const bool e3 = look_up();
+    bool ends = false;
+    if (e0) {
+#pragma unroll
+      for (int i = 0; i < (kKeys + 63) / 64; ++i) bad = bad || bad_pages[s4 * 2 + i];
+      const int p0 = w.t * kKeys;
+      const bool masked = p0 + kKeys > w.q.start;   // the step reaches the tree (or the end)
       if constexpr (DT != DFLASH_I8) {
         if (masked) {
           // A weight of zero times an infinity is no zero: a node's value that
           // is not finite must not reach the rows that do not see it.  Such
           // elements become zeros here and are added at the end, where seen.
-          unsigned char* vw = ta_smem + (t & 1) * 2 * S::kTile + S::kTile;
+          unsigned char* vw = stage + S::kTile;
           for (int x = tid; x < S::kTile / 16; x += S::kThreads) {
-            if (p0 + x / S::kChunks < q.start) continue;
-            u32x4 w = ld16(vw + x * 16);
-            if (odd_values<DT>(w)) {
+            if (p0 + x / S::kChunks < w.q.start) continue;
+            u32x4 v = ld16(vw + x * 16);
+            if (odd_values<DT>(v)) {
               odd = true;
-              st16(vw + x * 16, w);
+              st16(vw + x * 16, v);
             }
           }
           step_barrier();
         }
       }
+      const unsigned char* ks = stage;
+      const unsigned char* vs = stage + S::kTile;
 #pragma unroll
       for (int sub = 0; sub < S::kSubs; ++sub) {
         const int kb = (kw * S::kSubs + sub) * 32;  // first key of the block within the step
@@ -481,33 +585,32 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
             s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16<DT>(w[0], w[1]), qf[2 * t32], s, 0, 0, 0);
             s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16<DT>(w[2], w[3]), qf[2 * t32 + 1], s, 0, 0, 0);
           }
-          const float* kscale = scales + (t & 1) * 2 * kKeys + kb + 4 * half;
+          const float* kscale = scales + g * 2 * kKeys + kb + 4 * half;
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] *= kscale[8 * (i >> 2) + (i & 3)];
         }
         // s[i]: key 8 (i / 4) + 4 half + i % 4 of the block
         uint32_t vis = ~0u;
         if (masked) {
-          const int64_t k0 = p0 + kb;
-          const int pre = (int)min(max(q.start - k0, (int64_t)0), (int64_t)32);
-          const int64_t rel = k0 - q.start;         // the node of key 0 of the block
+          const int k0 = p0 + kb, rel = k0 - w.q.start;   // rel: the node of key 0 of the block
+          const int pre = min(max(-rel, 0), 32);
           uint32_t bits = 0;
-          int64_t seen = q.n;
+          int seen = w.q.n;
           if (!a.mask) {
-            seen = min(seen, (int64_t)node + 1);
+            seen = min(seen, node + 1);
             bits = ~0u;
-          } else if (rel < q.n && pre < 32) {
-            const uint64_t* mw = a.mask + (int64_t)(q.first + node) * a.mask_words;
+          } else if (rel < w.q.n && pre < 32) {
+            const uint64_t* mw = a.mask + (int64_t)(w.q.first + node) * a.mask_words;
             if (rel < 0) {
               bits = (uint32_t)(mw[0] << -rel);
             } else {
-              const int w = (int)(rel >> 6), sh = (int)(rel & 63);
-              uint64_t x = mw[w] >> sh;
-              if (sh > 32 && w + 1 < a.mask_words) x |= mw[w + 1] << (64 - sh);
+              const int word = rel >> 6, sh = rel & 63;
+              uint64_t x = mw[word] >> sh;
+              if (sh > 32 && word + 1 < a.mask_words) x |= mw[word + 1] << (64 - sh);
               bits = (uint32_t)x;
             }
           }
-          bits &= low_bits((int)min(max(seen - rel, (int64_t)0), (int64_t)32));
+          bits &= low_bits(seen - rel);
           vis = low_bits(pre) | (bits & ~low_bits(pre));
           vis >>= 4 * half;                         // now bit 8 (i / 4) + i % 4 for s[i]
 #pragma unroll
@@ -533,12 +636,12 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[i] = __builtin_amdgcn_exp2f(DT == DFLASH_BF16 ? fmaf(s[i], cs, -base) : s[i] - base);
+          s[i] = __builtin_amdgcn_exp2f(DT != DFLASH_I8 ? fmaf(s[i], cs, -base) : s[i] - base);
           sum += s[i];
         }
         l += sum;
         if constexpr (DT != DFLASH_BF16) {
-          const float* vscale = scales + (t & 1) * 2 * kKeys + kKeys + kb + 4 * half;
+          const float* vscale = scales + g * 2 * kKeys + kKeys + kb + 4 * half;
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] *= vscale[8 * (i >> 2) + (i & 3)];
           if (masked) {
@@ -598,159 +701,189 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
           }
         }
       }
-      step_barrier();                              // every wave is done with this stage
-      scale_now = scale_next;
-      if (t + 2 < t1) issue(t + 2);
+      ends = ++w.t == w.t1;
     }
-
-    // join the key waves: O of all but the first through LDS
-    l = half_sum(l);
-    float mc = m == -INFINITY ? -INFINITY : m * cs;
-    if constexpr (S::kKeyWaves > 1) {
-      float2* st = reinterpret_cast<float2*>(stats);
-      if (half == 0) st[kw * S::kRows + row] = make_float2(mc, l);
-      step_barrier();
-      float top = -INFINITY;
+    step_barrier();                                 // every wave is done with this stage; the addresses are there
+    if (ends) {
+      const JoinItem it = {0, 0, rows, w.q.first, w.q.n, w.q.start, w.req, w.head, w.tile, {0, 0, 0}};
+      const int t_last = w.t, steps = w.q.steps, out_node = node, out_gh = gh;
+      const int64_t item_at = w.at + kItemCost;
+      const bool item_bad = bad, item_odd = odd, whole = t_first == 0 && t_last == steps;
+      const int slot = item_at < piece.u0 ? 0 : 1;  // a cut item that began before the piece, or in it
+      float mc = m == -INFINITY ? -INFINITY : m * cs;
+      l = half_sum(l);
+      w.next_item(a, group);
+      if (w.valid) load_query();                    // arrives while this item is finished
+      // join the key waves, two halves at a time, through the free stage
+      if constexpr (S::kKeyWaves > 1) {
+        if (half == 0) stats[kw * S::kRows + row] = make_float2(mc, l);
+        step_barrier();
+        float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < S::kKeyWaves; ++i) top = fmaxf(top, st[i * S::kRows + row].x);
-      const float keep = mc == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mc - top);
-      l = 0.f;
+        for (int i = 0; i < S::kKeyWaves; ++i) top = fmaxf(top, stats[i * S::kRows + row].x);
+        const float keep = mc == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mc - top);
+        l = 0.f;
 #pragma unroll
-      for (int i = 0; i < S::kKeyWaves; ++i) {
-        const float2 x = st[i * S::kRows + row];
-        l += x.x == -INFINITY ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - top);
-      }
-      mc = top;
-      float4* pool = reinterpret_cast<float4*>(ta_smem) + rw * (D / 8) * 64 + lane;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[b][i] *= keep;
-      if (kw > 0) {
+        for (int i = 0; i < S::kKeyWaves; ++i) {
+          const float2 x = stats[i * S::kRows + row];
+          l += x.x == -INFINITY ? x.y : x.y * __builtin_amdgcn_exp2f(x.x - top);
+        }
+        mc = top;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            pool[((kw - 1) * RW * (D / 8) + 4 * b + i) * 64] =
-                make_float4(o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]);
-      }
-      step_barrier();
-      if (kw == 0) {
+          for (int i = 0; i < 16; ++i) o[b][i] *= keep;
 #pragma unroll
-        for (int x = 0; x < S::kKeyWaves - 1; ++x)
+        for (int from = S::kKeyWaves / 2; from > 0; from /= 2) {
+          float4* pool = reinterpret_cast<float4*>(stage) + ((kw % from) * RW + rw) * (D / 8) * 64 + lane;
+          if (kw >= from && kw < 2 * from) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pool[(4 * b + i) * 64] = make_float4(o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]);
+          }
+          step_barrier();
+          if (kw < from) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = pool[(4 * b + i) * 64];
+                o[b][4 * i] += f.x;
+                o[b][4 * i + 1] += f.y;
+                o[b][4 * i + 2] += f.z;
+                o[b][4 * i + 3] += f.w;
+              }
+          }
+          step_barrier();
+        }
+      }
+      if (item_bad) l = __builtin_nanf("");         // every thread has seen every step's pages
+      const bool any_odd = DT != DFLASH_I8 && __syncthreads_or(item_odd);
+      if (kw == 0 && row < it.rows) {
+        if (whole) {
+          const float inv = sees_any(a, it.first, it.nodes, it.start, out_node) ? 1.f / l : 0.f;
+          uint16_t* op = a.out + ((int64_t)(it.first + out_node) * a.n_q_heads + it.head * group + out_gh) * D;
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = pool[(x * RW * (D / 8) + 4 * b + i) * 64];
-              o[b][4 * i] += f.x;
-              o[b][4 * i + 1] += f.y;
-              o[b][4 * i + 2] += f.z;
-              o[b][4 * i + 3] += f.w;
-            }
-      }
-    }
-    if (__syncthreads_or(bad)) l = __builtin_nanf("");
-    const bool any_odd = DT != DFLASH_I8 && __syncthreads_or(odd);
-    if (kw == 0 && row < rows) {
-      if (whole) {
-        const float inv = sees_any(a, q, node) ? 1.f / l : 0.f;
-        uint16_t* op = a.out + ((int64_t)(q.first + node) * a.n_q_heads + head * group + gh) * D;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint2*>(op + 32 * b + 8 * i + 4 * half) =
-                make_uint2(pack_bf16(o[b][4 * i] * inv, o[b][4 * i + 1] * inv),
-                           pack_bf16(o[b][4 * i + 2] * inv, o[b][4 * i + 3] * inv));
-        if (any_odd) {
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint2*>(op + 32 * b + 8 * i + 4 * half) =
+                  make_uint2(pack_bf16(o[b][4 * i] * inv, o[b][4 * i + 1] * inv),
+                             pack_bf16(o[b][4 * i + 2] * inv, o[b][4 * i + 3] * inv));
+          if (any_odd) {
 #pragma unroll 1
-          for (int x = 0; x < D / 8; ++x) {         // this lane's own 4 elements of each 8
-            uint2* at = reinterpret_cast<uint2*>(op + 8 * x + 4 * half);
-            const uint2 w = *at;
-            float f[4] = {bf16_to_f32(w.x & 0xffffu), bf16_to_f32(w.x >> 16), bf16_to_f32(w.y & 0xffffu), bf16_to_f32(w.y >> 16)};
-            add_odd<DT, D>(a, q, req, head, node, 8 * x + 4 * half, f);
-            *at = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+            for (int x = 0; x < D / 8; ++x) {       // this lane's own 4 elements of each 8
+              uint2* at = reinterpret_cast<uint2*>(op + 8 * x + 4 * half);
+              const uint2 v = *at;
+              float f[4] = {bf16_to_f32(v.x & 0xffffu), bf16_to_f32(v.x >> 16), bf16_to_f32(v.y & 0xffffu),
+                            bf16_to_f32(v.y >> 16)};
+              add_odd<DT, D>(a, it.first, it.nodes, it.start, it.req, it.head, out_node, 8 * x + 4 * half, f);
+              *at = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+            }
+          }
+        } else {
+          float* part = parts + slot * S::kPartFloats;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(part + row * D + 32 * b + 8 * i + 4 * half) =
+                  make_float4(o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]);
+          if (half == 0) *reinterpret_cast<float2*>(part + S::kRows * D + 2 * row) = make_float2(mc, l);
+          if (tid == 0) {
+            part[S::kPartOdd] = any_odd ? 1.f : 0.f;
+            JoinItem j = it;
+            j.piece = piece.of(item_at);
+            j.n = piece.of(item_at + steps - 1) - j.piece + 1;
+            joins[piece.w * 2 + slot] = j;
           }
         }
-      } else {
-        float* part = static_cast<float*>(a.workspace) + ((int64_t)piece.w * 2 + (first_item ? 0 : 1)) * S::kPartFloats;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(part + row * D + 32 * b + 8 * i + 4 * half) =
-                make_float4(o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]);
-        if (half == 0) *reinterpret_cast<float2*>(part + S::kRows * D + 2 * row) = make_float2(mc, l);
-        if (tid == 0) part[S::kPartOdd] = any_odd ? 1.f : 0.f;
       }
+      clear();
+      step_barrier();                               // the stage and the statistics are free
     }
-    u += t1 - t0;
+    // Past the last step the same number of loads takes row 0 of the pool (into
+    // a stage that nothing reads any more): at the loop's top, on every path,
+    // all but these are older than the count waited for, and the compiler adds
+    // no waits of its own at the other loads' uses.
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int blk = i * S::kWaves + wave, r = blk * (1024 / kRB) + lrow;
+      const int64_t off = row_at[g * kKeys + r] + ((lslot ^ S::swizzle(r)) << 4);
+      __builtin_amdgcn_global_load_lds((const void*)(c.k + off), (lds_void_t*)(stage + blk * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(c.v + off), (lds_void_t*)(stage + S::kTile + blk * 1024), 16, 0, 0);
+    }
+    e0 = e1;
+    e1 = e2;
+    e2 = e3;
+    if (!(e0 || e1 || e2)) break;
   }
+  wait_vm<0>();
 }
 
 // Joins the pieces of cut items.  The workgroups of an item's pieces share its
-// rows; the pieces are summed in the order of the line, so the result does not
-// depend on which finished first.
+// rows: 256 threads take as many groups of pieces as there are (up to 16) of
+// 256 / groups vectors of the result, and the groups' sums are added in their
+// order, so nothing depends on which piece finished first.
 template <int DT, int D, int RW>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, FastDiv per_group) {
   using S = Shape<DT, D, RW>;
-  const Piece piece = find_piece<256>(a, S::kKeys, S::kRows, per_group.d);
-  if (piece.w >= piece.pieces) return;
-  const KvView& c = a.c;
-  const int group = per_group.d;
-  int req = piece.req;
-  int64_t req_begin = piece.before, u = piece.u0;
-  while (u < piece.u1) {
-    const Req q = request(a, req, S::kKeys, S::kRows, group);
-    const int64_t req_units = (int64_t)q.steps * q.tiles * c.n_kv_heads;
-    if (u >= req_begin + req_units) {
-      req_begin += req_units;
-      ++req;
-      continue;
-    }
-    const int32_t item = (int32_t)((u - req_begin) / q.steps);
-    const int64_t i0 = req_begin + (int64_t)item * q.steps, i1 = i0 + q.steps;
-    u = i1;
-    if (i0 >= piece.u0 && i1 <= piece.u1) {        // whole: on to the piece's last item
-      const int64_t skip = (min(piece.u1, req_begin + req_units) - i1) / q.steps;
-      u += skip * q.steps;
-      continue;
-    }
-    const int first = piece.of(i0), last = piece.of(i1 - 1), n = last - first + 1;
-    const int head = item / q.tiles, tile = item - head * q.tiles;
-    const int rows = min(S::kRows, q.n * group - tile * S::kRows);
-    const float* parts = static_cast<const float*>(a.workspace);
-    const bool first_starts = piece.begin(first) == i0;
-    auto part = [&](int x) {
-      const int slot = x == 0 && !first_starts ? 1 : 0;
-      return parts + ((int64_t)(first + x) * 2 + slot) * S::kPartFloats;
-    };
-    for (int e = (piece.w - first) * 256 + (int)threadIdx.x; e < rows * (D / 4); e += n * 256) {
-      const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-      float top = -INFINITY;
-      for (int x = 0; x < n; ++x) top = fmaxf(top, part(x)[S::kRows * D + 2 * row]);
-      float l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-      for (int x = 0; x < n; ++x) {
-        const float* p = part(x);
+  __shared__ float sh[256][7];
+  const JoinItem* joins = static_cast<const JoinItem*>(a.workspace);
+  const float* parts = reinterpret_cast<const float*>(joins + 2 * gridDim.x);
+  const int tid = threadIdx.x, group = per_group.d;
+  for (int slot = 0; slot < 2; ++slot) {
+    const JoinItem it = joins[blockIdx.x * 2 + slot];
+    if (it.n == 0) continue;
+    const int groups = it.n > 8 ? 16 : it.n > 4 ? 8 : it.n > 2 ? 4 : 2, vecs = 256 / groups;
+    const int mine = tid / vecs, total = it.rows * (D / 4);
+    for (int v0 = ((int)blockIdx.x - it.piece) * vecs; v0 < total; v0 += it.n * vecs) {
+      const int e = min(v0 + tid % vecs, total - 1), row = e / (D / 4), d = (e % (D / 4)) * 4;
+      float top = -INFINITY, l = 0.f, odd = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+      auto add = [&](float m2, float l2, float a0, float a1, float a2, float a3) {
+        const float next = fmaxf(top, m2);
+        // a part that saw nothing has l = 0, or NaN for a bad page, and O = 0
+        const float w1 = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(top - next);
+        const float w2 = m2 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m2 - next);
+        top = next;
+        l = l * w1 + l2 * w2;
+        o0 = o0 * w1 + a0 * w2;
+        o1 = o1 * w1 + a1 * w2;
+        o2 = o2 * w1 + a2 * w2;
+        o3 = o3 * w1 + a3 * w2;
+      };
+#pragma unroll 4
+      for (int x = mine; x < it.n; x += groups) {
+        const float* p = parts + ((int64_t)(it.piece + x) * 2 + (x == 0 ? 1 : 0)) * S::kPartFloats;
         const float2 ml = *reinterpret_cast<const float2*>(p + S::kRows * D + 2 * row);
         const float4 f = *reinterpret_cast<const float4*>(p + row * D + d);
-        const float w = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-        l += ml.x == -INFINITY ? ml.y : ml.y * w;   // a part that saw nothing has l = 0, or NaN for a bad page
-        o0 = fmaf(f.x, w, o0);
-        o1 = fmaf(f.y, w, o1);
-        o2 = fmaf(f.z, w, o2);
-        o3 = fmaf(f.w, w, o3);
+        odd += p[S::kPartOdd];
+        add(ml.x, ml.y, f.x, f.y, f.z, f.w);
       }
-      const int flat = tile * S::kRows + row, node = per_group.div(flat), gh = flat - node * group;
-      const float inv = sees_any(a, q, node) ? 1.f / l : 0.f;
+      __syncthreads();
+      sh[tid][0] = top;
+      sh[tid][1] = l;
+      sh[tid][2] = o0;
+      sh[tid][3] = o1;
+      sh[tid][4] = o2;
+      sh[tid][5] = o3;
+      sh[tid][6] = odd;
+      __syncthreads();
+      if (mine != 0 || v0 + tid >= total) continue;
+      for (int x = 1; x < groups; ++x) {
+        const float(&f)[7] = sh[x * vecs + tid];
+        odd += f[6];
+        add(f[0], f[1], f[2], f[3], f[4], f[5]);
+      }
+      const int flat = it.tile * S::kRows + row, node = per_group.div(flat), gh = flat - node * group;
+      const float inv = sees_any(a, it.first, it.nodes, it.start, node) ? 1.f / l : 0.f;
       float f[4] = {o0 * inv, o1 * inv, o2 * inv, o3 * inv};
       if constexpr (DT != DFLASH_I8) {
-        bool odd = false;
-        for (int x = 0; x < n; ++x) odd = odd || part(x)[S::kPartOdd] != 0.f;
-        if (odd) add_odd<DT, D>(a, q, req, head, node, d, f);
+        if (odd != 0.f) add_odd<DT, D>(a, it.first, it.nodes, it.start, it.req, it.head, node, d, f);
       }
-      *reinterpret_cast<uint2*>(a.out + ((int64_t)(q.first + node) * a.n_q_heads + head * group + gh) * D + d) =
+      *reinterpret_cast<uint2*>(a.out + ((int64_t)(it.first + node) * a.n_q_heads + it.head * group + gh) * D + d) =
           make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
     }
   }
@@ -766,7 +899,7 @@ template <int DT, int D, int RW>
 struct Launch {
   using S = Shape<DT, D, RW>;
   static int grid() { return 256 * S::kPerCu; }
-  static size_t bytes() { return (size_t)grid() * 2 * S::kPartFloats * sizeof(float); }
+  static size_t bytes() { return (size_t)grid() * 2 * (sizeof(JoinItem) + S::kPartFloats * sizeof(float)); }
   static hipError_t run(const TreeArgs& a, hipStream_t s) {
     const FastDiv per_group = FastDiv::make(a.n_q_heads / a.c.n_kv_heads);
     tree_attention_kernel<DT, D, RW><<<grid(), S::kThreads, S::kLds, s>>>(a, per_group);
