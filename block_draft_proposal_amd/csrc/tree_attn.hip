@@ -28,6 +28,8 @@
 // Loads run two steps ahead of the products and do not stop at an item's end:
 // each step's rows are looked up (page table, then addresses into LDS) by one
 // thread a row, two steps before its direct loads are issued.
+#include <type_traits>
+
 #include "kv_cache.h"
 
 namespace dflash {
@@ -60,18 +62,22 @@ struct Shape {
   static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;                 // workgroups of a CU
   static constexpr int kPartOdd = kRows * (D + 2);                         // a partial: O [kRows][D], m and l of each
   static constexpr int kPartFloats = kPartOdd + 4;                         // row, whether odd values were left out
-  static_assert(kSubs >= 1 && kLoads >= 1 && kTile % (1024 * kWaves) == 0, "a step splits over the waves");
+  static_assert(kSubs >= 1 && kSubs <= 4 && kLoads >= 1 && kTile % (1024 * kWaves) == 0, "a step splits over the waves");
   static_assert(kKeyWaves / 2 * kRows * D * 4 <= 2 * kTile, "the join fits where one stage was");
   static_assert(kKeys <= kThreads && kKeys <= 128, "one thread looks up a row");
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
 
-  // Chunk c of stage row r lies in slot c ^ swizzle(r).  8 lanes of a 16-byte
-  // read (8 consecutive rows, one chunk) and 16 lanes of a transposed read
-  // (rows r .. r+3 and two chunks of 16-bit elements; r .. r+3, r+8 .. r+11
-  // and one chunk of 8-bit ones) fall on different banks.
-  __device__ static __forceinline__ int swizzle(int r) {
-    if constexpr (DT == DFLASH_BF16) return kRowBytes == 128 ? ((r >> 1) & 3) << 1 : (r & 7) << 1;
-    else return kRowBytes == 256 ? r & 15 : kRowBytes == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+  // Chunk c of stage row r lies in slot c ^ swizzle(r), so that reads of one
+  // instruction fall on different banks: for K, 16 consecutive rows of one
+  // chunk; for V's transposed reads, rows r .. r+3 of four chunks (16-bit
+  // elements) or rows r .. r+3, r+8 .. r+11 of two (8-bit).
+  static constexpr int kRowsPerBanks = kRowBytes >= 256 ? 1 : 256 / kRowBytes;
+  __device__ static __forceinline__ int k_swizzle(int r) { return (r / kRowsPerBanks) & (16 / kRowsPerBanks - 1); }
+  __device__ static __forceinline__ int v_swizzle(int r) {
+    if constexpr (DT == DFLASH_BF16) return kRowBytes == 128 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+    else if constexpr (kRowBytes == 256) return ((r & 3) | ((r >> 1) & 4)) << 1;
+    else if constexpr (kRowBytes == 128) return (((r >> 1) & 1) | ((r >> 2) & 2)) << 1;
+    else return ((r >> 3) & 1) << 1;
   }
 };
 
@@ -134,42 +140,98 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char*)p;
 }
 
-// Transposed reads of V at LDS addresses a[i] + O0 and a[i] + O1: among 16
-// lanes, lane i gets column i of the 16 x 16-bit by 4-row (8-bit: 8-row) block
-// whose pieces of 8 bytes the lanes address.  One block of assembly with its
-// own wait: the compiler takes the builtins to depend on every direct load in
+// Transposed reads of V at LDS addresses a[i] + O0 + j STEP: among 16 lanes,
+// lane i gets column i of the 16 x 16-bit by 4-row (8-bit: 8-row) block whose
+// pieces of 8 bytes the lanes address.  One block of assembly with its own
+// wait: the compiler takes the builtins to depend on every direct load in
 // flight and would wait for the next step's.
-template <bool WIDE, int O0, int O1>
+template <bool WIDE, int O0, int STEP>
+__device__ __forceinline__ void read_transposed(const uint32_t (&a)[4], i32x2_t (&r)[4][4]) {
+  if constexpr (WIDE)
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %16 offset:%20\n\t" "ds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %2, %16 offset:%22\n\t" "ds_read_b64_tr_b16 %3, %16 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %4, %17 offset:%20\n\t" "ds_read_b64_tr_b16 %5, %17 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %6, %17 offset:%22\n\t" "ds_read_b64_tr_b16 %7, %17 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %8, %18 offset:%20\n\t" "ds_read_b64_tr_b16 %9, %18 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %10, %18 offset:%22\n\t" "ds_read_b64_tr_b16 %11, %18 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %12, %19 offset:%20\n\t" "ds_read_b64_tr_b16 %13, %19 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %14, %19 offset:%22\n\t" "ds_read_b64_tr_b16 %15, %19 offset:%23\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[2][2]), "=&v"(r[2][3]), "=&v"(r[3][0]), "=&v"(r[3][1]), "=&v"(r[3][2]), "=&v"(r[3][3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
+  else
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %16 offset:%20\n\t" "ds_read_b64_tr_b8 %1, %16 offset:%21\n\t"
+        "ds_read_b64_tr_b8 %2, %16 offset:%22\n\t" "ds_read_b64_tr_b8 %3, %16 offset:%23\n\t"
+        "ds_read_b64_tr_b8 %4, %17 offset:%20\n\t" "ds_read_b64_tr_b8 %5, %17 offset:%21\n\t"
+        "ds_read_b64_tr_b8 %6, %17 offset:%22\n\t" "ds_read_b64_tr_b8 %7, %17 offset:%23\n\t"
+        "ds_read_b64_tr_b8 %8, %18 offset:%20\n\t" "ds_read_b64_tr_b8 %9, %18 offset:%21\n\t"
+        "ds_read_b64_tr_b8 %10, %18 offset:%22\n\t" "ds_read_b64_tr_b8 %11, %18 offset:%23\n\t"
+        "ds_read_b64_tr_b8 %12, %19 offset:%20\n\t" "ds_read_b64_tr_b8 %13, %19 offset:%21\n\t"
+        "ds_read_b64_tr_b8 %14, %19 offset:%22\n\t" "ds_read_b64_tr_b8 %15, %19 offset:%23\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[2][2]), "=&v"(r[2][3]), "=&v"(r[3][0]), "=&v"(r[3][1]), "=&v"(r[3][2]), "=&v"(r[3][3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
+}
+template <bool WIDE, int O0, int STEP>
 __device__ __forceinline__ void read_transposed(const uint32_t (&a)[4], i32x2_t (&r)[4][2]) {
   if constexpr (WIDE)
     asm volatile(
-        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\tds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %2, %9 offset:%12\n\tds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %4, %10 offset:%12\n\tds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %6, %11 offset:%12\n\tds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t" "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t" "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t" "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t" "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
         "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]),
-          "=&v"(r[3][0]), "=&v"(r[3][1])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O1));
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[3][0]), "=&v"(r[3][1])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP));
   else
     asm volatile(
-        "ds_read_b64_tr_b8 %0, %8 offset:%12\n\tds_read_b64_tr_b8 %1, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %2, %9 offset:%12\n\tds_read_b64_tr_b8 %3, %9 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %4, %10 offset:%12\n\tds_read_b64_tr_b8 %5, %10 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %6, %11 offset:%12\n\tds_read_b64_tr_b8 %7, %11 offset:%13\n\t"
+        "ds_read_b64_tr_b8 %0, %8 offset:%12\n\t" "ds_read_b64_tr_b8 %1, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b8 %2, %9 offset:%12\n\t" "ds_read_b64_tr_b8 %3, %9 offset:%13\n\t"
+        "ds_read_b64_tr_b8 %4, %10 offset:%12\n\t" "ds_read_b64_tr_b8 %5, %10 offset:%13\n\t"
+        "ds_read_b64_tr_b8 %6, %11 offset:%12\n\t" "ds_read_b64_tr_b8 %7, %11 offset:%13\n\t"
         "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]),
-          "=&v"(r[3][0]), "=&v"(r[3][1])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O1));
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[3][0]), "=&v"(r[3][1])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP));
 }
-template <int O0, int O1>
-__device__ __forceinline__ void read_transposed_8bit(const uint32_t (&a)[2], i32x2_t (&r)[2][2]) {
-  asm volatile(
-      "ds_read_b64_tr_b8 %0, %4 offset:%6\n\tds_read_b64_tr_b8 %1, %4 offset:%7\n\t"
-      "ds_read_b64_tr_b8 %2, %5 offset:%6\n\tds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
-      : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O1));
+template <bool WIDE, int O0, int STEP>
+__device__ __forceinline__ void read_transposed(const uint32_t (&a)[2], i32x2_t (&r)[2][4]) {
+  if constexpr (WIDE)
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%10\n\t" "ds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
+        "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t" "ds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %4, %9 offset:%10\n\t" "ds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
+        "ds_read_b64_tr_b16 %6, %9 offset:%12\n\t" "ds_read_b64_tr_b16 %7, %9 offset:%13\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3])
+        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
+  else
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %8 offset:%10\n\t" "ds_read_b64_tr_b8 %1, %8 offset:%11\n\t"
+        "ds_read_b64_tr_b8 %2, %8 offset:%12\n\t" "ds_read_b64_tr_b8 %3, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b8 %4, %9 offset:%10\n\t" "ds_read_b64_tr_b8 %5, %9 offset:%11\n\t"
+        "ds_read_b64_tr_b8 %6, %9 offset:%12\n\t" "ds_read_b64_tr_b8 %7, %9 offset:%13\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3])
+        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
+}
+template <bool WIDE, int O0, int STEP>
+__device__ __forceinline__ void read_transposed(const uint32_t (&a)[2], i32x2_t (&r)[2][2]) {
+  if constexpr (WIDE)
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%6\n\t" "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
+        "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t" "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
+        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP));
+  else
+    asm volatile(
+        "ds_read_b64_tr_b8 %0, %4 offset:%6\n\t" "ds_read_b64_tr_b8 %1, %4 offset:%7\n\t"
+        "ds_read_b64_tr_b8 %2, %5 offset:%6\n\t" "ds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
+        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP));
 }
 
 // Sets the elements of w that are not finite to zero; whether there were any.
@@ -444,13 +506,13 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_I8 ? 1.f : c2;
 
   // K reads: row l32 of a 32-key block, chunk 2t + half in slot (2t) ^ kx
-  const int kx = half ^ S::swizzle(l32);
+  const int kx = half ^ S::k_swizzle(l32);
   // V reads: lane i of a 16-lane group addresses row vr of a 16-key block
   // (plus 8 for the second half of 16-bit ones) and 8 bytes of a 16-column block
   const int g16 = lane >> 4, i16 = lane & 15;
   const int vj = DT == DFLASH_BF16 ? i16 >> 2 : i16 >> 1;
   const int vr = DT == DFLASH_BF16 ? 4 * half + vj : 8 * (vj >> 2) + 4 * half + (vj & 3);
-  const int vx = (DT == DFLASH_BF16 ? 2 * (g16 & 1) + ((i16 >> 1) & 1) : g16 & 1) ^ S::swizzle(vr);
+  const int vx = (DT == DFLASH_BF16 ? 2 * (g16 & 1) + ((i16 >> 1) & 1) : g16 & 1) ^ S::v_swizzle(vr);
   const int vbase = vr * kRB + (i16 & 1) * 8;
   // direct loads: lane's row of a 1 KB block, and its chunk's place in the row
   // (the swizzle of a row repeats from block to block of a wave or is taken per load)
@@ -512,6 +574,158 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   load_query();
   clear();
 
+  // The products of a step with this wave's rows and keys, 32 keys at a time.
+  // masked: some of the keys are nodes, or past the end.  The scores of the
+  // next 32 keys (matrix cores) run under the exponentials of these.
+  auto products = [&](const unsigned char* stage, int g, int p0, bool masked) {
+    const int kb0 = kw * S::kSubs * 32;             // first key of this wave
+    const unsigned char* krow = stage + (kb0 + l32) * kRB;
+    const uint32_t v0 = lds_address(stage + S::kTile + kb0 * kRB) + vbase;
+    u32x4 kf[kRB / 32];
+    auto read_keys = [&](int sub) {
+#pragma unroll
+      for (int i = 0; i < kRB / 32; ++i) kf[i] = ld16(krow + sub * 32 * kRB + (((2 * i) ^ kx) << 4));
+    };
+    auto scores = [&](f32x16_t& s) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      if constexpr (DT == DFLASH_BF16) {
+#pragma unroll
+        for (int t16 = 0; t16 < kSteps16; ++t16)
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, kf[t16]), qf[t16], s, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int t32 = 0; t32 < kSteps16 / 2; ++t32) {
+          const u32x4 x = kf[t32];
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16<DT>(x[0], x[1]), qf[2 * t32], s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16<DT>(x[2], x[3]), qf[2 * t32 + 1], s, 0, 0, 0);
+        }
+      }
+    };
+    read_keys(0);
+    f32x16_t s;
+    scores(s);
+#pragma unroll
+    for (int sub = 0; sub < S::kSubs; ++sub) {
+      // s[i]: key 8 (i / 4) + 4 half + i % 4 of the block of 32
+      if constexpr (DT != DFLASH_BF16) {
+        const float* kscale = scales + g * 2 * kKeys + kb0 + sub * 32 + 4 * half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= kscale[8 * (i >> 2) + (i & 3)];
+      }
+      uint32_t vis = ~0u;
+      if (masked) {
+        const int k0 = p0 + kb0 + sub * 32, rel = k0 - w.q.start;   // rel: the node of key 0 of the block
+        const int pre = min(max(-rel, 0), 32);
+        uint32_t bits = 0;
+        int seen = w.q.n;
+        if (!a.mask) {
+          seen = min(seen, node + 1);
+          bits = ~0u;
+        } else if (rel < w.q.n && pre < 32) {
+          const uint64_t* mw = a.mask + (int64_t)(w.q.first + node) * a.mask_words;
+          if (rel < 0) {
+            bits = (uint32_t)(mw[0] << -rel);
+          } else {
+            const int word = rel >> 6, sh = rel & 63;
+            uint64_t x = mw[word] >> sh;
+            if (sh > 32 && word + 1 < a.mask_words) x |= mw[word + 1] << (64 - sh);
+            bits = (uint32_t)x;
+          }
+        }
+        bits &= low_bits(seen - rel);
+        vis = (low_bits(pre) | (bits & ~low_bits(pre))) >> (4 * half);   // bit 8 (i / 4) + i % 4 for s[i]
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = (vis >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : -INFINITY;
+      }
+      float top = s[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+      top = half_max(top);
+      // The sums keep the maximum they were built with until a row's passes it
+      // by 2^8: weights up to 256 are as exact as those up to 1, and most
+      // blocks then leave O alone.
+      if (__any((top - m) * cs > 8.f)) {
+        const float next = fmaxf(m, top), keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - next) * cs);
+        m = next;
+        l *= keep;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+      }
+      const float base = m == -INFINITY ? 0.f : m * cs;
+      if (sub + 1 < S::kSubs) read_keys(sub + 1);
+      // V of up to four blocks of 32 columns: [column block][16-key operand]
+      constexpr int kGroup = kBlocks < 4 ? kBlocks : 4, kPieces = DT == DFLASH_BF16 ? 4 : 2;
+      i32x2_t r[kGroup][kPieces];
+      auto read_v = [&](int b, auto sub_c) {
+        uint32_t at[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) at[i] = v0 + (uint32_t)(((kPerBlock * (b + i)) ^ vx) << 4);
+        read_transposed<DT == DFLASH_BF16, decltype(sub_c)::value * 32 * kRB, (DT == DFLASH_BF16 ? 8 : 16) * kRB>(at, r);
+      };
+      auto read_group = [&](int b) {
+        if (sub == 0) read_v(b, std::integral_constant<int, 0>());
+        else if (sub == 1) read_v(b, std::integral_constant<int, 1>());
+        else if (sub == 2) read_v(b, std::integral_constant<int, 2>());
+        else read_v(b, std::integral_constant<int, 3>());
+      };
+      read_group(0);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x16_t next_s;
+      if (sub + 1 < S::kSubs) scores(next_s);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(DT != DFLASH_I8 ? fmaf(s[i], cs, -base) : s[i] - base);
+        sum += s[i];
+      }
+      l += sum;
+      if constexpr (DT != DFLASH_BF16) {
+        const float* vscale = scales + g * 2 * kKeys + kKeys + kb0 + sub * 32 + 4 * half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= vscale[8 * (i >> 2) + (i & 3)];
+        if (masked) {                               // 0 * NaN: an unseen key's scale
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = (vis >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : 0.f;
+        }
+      }
+      // weights rounded to bf16 (half a step, 2^-8 of each): the product with
+      // V is bf16 x bf16 on the matrix cores; l sums them unrounded
+      bf16x8_t pf[2];
+#pragma unroll
+      for (int u16 = 0; u16 < 2; ++u16) {
+        const u32x4 pw = {pack_bf16(s[8 * u16], s[8 * u16 + 1]), pack_bf16(s[8 * u16 + 2], s[8 * u16 + 3]),
+                          pack_bf16(s[8 * u16 + 4], s[8 * u16 + 5]), pack_bf16(s[8 * u16 + 6], s[8 * u16 + 7])};
+        pf[u16] = __builtin_bit_cast(bf16x8_t, pw);
+      }
+      if (sub + 1 < S::kSubs) {
+#pragma unroll
+        for (int i = 0; i < kSteps16; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, (DT == DFLASH_BF16 ? 56 : DT == DFLASH_E4M3 ? 104 : 168) / kSteps16, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < kBlocks; b += kGroup) {
+        if (b) read_group(b);
+#pragma unroll
+        for (int x = 0; x < 2 * kGroup; ++x) {
+          const int i = x % kGroup, u16 = x / kGroup;
+          bf16x8_t vf;
+          if constexpr (DT == DFLASH_BF16)
+            vf = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(r[i][2 * u16], r[i][2 * u16 + 1], 0, 1, 2, 3));
+          else
+            vf = codes_to_bf16<DT>((uint32_t)r[i][u16][0], (uint32_t)r[i][u16][1]);
+          o[b + i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u16], o[b + i], 0, 0, 0);
+        }
+      }
+      if (sub + 1 < S::kSubs) s = next_s;
+    }
+  };
+
   // e0, e1, e2: whether steps g, g+1, g+2 exist.  Iteration g multiplies step
   // g, writes step g+1's scales, gives step g+2 its addresses and its direct
   // loads, and looks up step g+3's pages; the first two only fill.
@@ -563,144 +777,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
           step_barrier();
         }
       }
-      const unsigned char* ks = stage;
-      const unsigned char* vs = stage + S::kTile;
-#pragma unroll
-      for (int sub = 0; sub < S::kSubs; ++sub) {
-        const int kb = (kw * S::kSubs + sub) * 32;  // first key of the block within the step
-        f32x16_t s;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.f;
-        const unsigned char* krow = ks + (kb + l32) * kRB;
-        if constexpr (DT == DFLASH_BF16) {
-#pragma unroll
-          for (int t16 = 0; t16 < kSteps16; ++t16) {
-            const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, ld16(krow + (((2 * t16) ^ kx) << 4)));
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[t16], s, 0, 0, 0);
-          }
-        } else {
-#pragma unroll
-          for (int t32 = 0; t32 < kSteps16 / 2; ++t32) {
-            const u32x4 w = ld16(krow + (((2 * t32) ^ kx) << 4));
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16<DT>(w[0], w[1]), qf[2 * t32], s, 0, 0, 0);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16<DT>(w[2], w[3]), qf[2 * t32 + 1], s, 0, 0, 0);
-          }
-          const float* kscale = scales + g * 2 * kKeys + kb + 4 * half;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] *= kscale[8 * (i >> 2) + (i & 3)];
-        }
-        // s[i]: key 8 (i / 4) + 4 half + i % 4 of the block
-        uint32_t vis = ~0u;
-        if (masked) {
-          const int k0 = p0 + kb, rel = k0 - w.q.start;   // rel: the node of key 0 of the block
-          const int pre = min(max(-rel, 0), 32);
-          uint32_t bits = 0;
-          int seen = w.q.n;
-          if (!a.mask) {
-            seen = min(seen, node + 1);
-            bits = ~0u;
-          } else if (rel < w.q.n && pre < 32) {
-            const uint64_t* mw = a.mask + (int64_t)(w.q.first + node) * a.mask_words;
-            if (rel < 0) {
-              bits = (uint32_t)(mw[0] << -rel);
-            } else {
-              const int word = rel >> 6, sh = rel & 63;
-              uint64_t x = mw[word] >> sh;
-              if (sh > 32 && word + 1 < a.mask_words) x |= mw[word + 1] << (64 - sh);
-              bits = (uint32_t)x;
-            }
-          }
-          bits &= low_bits(seen - rel);
-          vis = low_bits(pre) | (bits & ~low_bits(pre));
-          vis >>= 4 * half;                         // now bit 8 (i / 4) + i % 4 for s[i]
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] = (vis >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : -INFINITY;
-        }
-        float top = s[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-        top = half_max(top);
-        // The sums keep the maximum they were built with until a row's passes
-        // it by 2^8: weights up to 256 are as exact as those up to 1, and most
-        // blocks then leave O alone.
-        if (__any((top - m) * cs > 8.f)) {
-          const float next = fmaxf(m, top), keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - next) * cs);
-          m = next;
-          l *= keep;
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[b][i] *= keep;
-        }
-        const float base = m == -INFINITY ? 0.f : m * cs;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[i] = __builtin_amdgcn_exp2f(DT != DFLASH_I8 ? fmaf(s[i], cs, -base) : s[i] - base);
-          sum += s[i];
-        }
-        l += sum;
-        if constexpr (DT != DFLASH_BF16) {
-          const float* vscale = scales + g * 2 * kKeys + kKeys + kb + 4 * half;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[i] *= vscale[8 * (i >> 2) + (i & 3)];
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = (vis >> (8 * (i >> 2) + (i & 3))) & 1 ? s[i] : 0.f;
-          }
-        }
-        const unsigned char* vblk = vs + kb * kRB;
-        // weights rounded to bf16 (half a step, 2^-8 of each): the product with
-        // V is bf16 x bf16 on the matrix cores; l sums them unrounded
-        bf16x8_t pf[2];
-#pragma unroll
-        for (int u16 = 0; u16 < 2; ++u16) {
-          const u32x4 pw = {pack_bf16(s[8 * u16], s[8 * u16 + 1]), pack_bf16(s[8 * u16 + 2], s[8 * u16 + 3]),
-                            pack_bf16(s[8 * u16 + 4], s[8 * u16 + 5]), pack_bf16(s[8 * u16 + 6], s[8 * u16 + 7])};
-          pf[u16] = __builtin_bit_cast(bf16x8_t, pw);
-        }
-        const uint32_t v0 = lds_address(vblk) + vbase;
-        auto v_at = [&](int b) { return v0 + (uint32_t)(((kPerBlock * b) ^ vx) << 4); };   // column block b, first keys
-        auto add = [&](int b, int u16, bf16x8_t vf) {
-          o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[u16], o[b], 0, 0, 0);
-        };
-        auto join16 = [](const i32x2_t (&r)[2]) {
-          return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3));
-        };
-        auto codes = [](i32x2_t r) { return codes_to_bf16<DT>((uint32_t)r[0], (uint32_t)r[1]); };
-        i32x2_t r[4][2];
-        if constexpr (DT == DFLASH_BF16 && D == 64) {
-          const uint32_t at[4] = {v_at(0), v_at(1), v_at(0) + 16 * kRB, v_at(1) + 16 * kRB};
-          read_transposed<true, 0, 8 * kRB>(at, r);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) add(i & 1, i >> 1, join16(r[i]));
-        } else if constexpr (DT == DFLASH_BF16) {
-#pragma unroll
-          for (int b = 0; b < kBlocks; b += 4) {
-            const uint32_t at[4] = {v_at(b), v_at(b + 1), v_at(b + 2), v_at(b + 3)};
-            read_transposed<true, 0, 8 * kRB>(at, r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) add(b + i, 0, join16(r[i]));
-            read_transposed<true, 16 * kRB, 24 * kRB>(at, r);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) add(b + i, 1, join16(r[i]));
-          }
-        } else if constexpr (D == 64) {
-          const uint32_t at[2] = {v_at(0), v_at(1)};
-          i32x2_t r2[2][2];
-          read_transposed_8bit<0, 16 * kRB>(at, r2);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) add(i >> 1, i & 1, codes(r2[i >> 1][i & 1]));
-        } else {
-#pragma unroll
-          for (int b = 0; b < kBlocks; b += 4) {
-            const uint32_t at[4] = {v_at(b), v_at(b + 1), v_at(b + 2), v_at(b + 3)};
-            read_transposed<false, 0, 16 * kRB>(at, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) add(b + (i >> 1), i & 1, codes(r[i >> 1][i & 1]));
-          }
-        }
-      }
+      products(stage, g, p0, masked);
       ends = ++w.t == w.t1;
     }
     step_barrier();                                 // every wave is done with this stage; the addresses are there
@@ -811,9 +888,11 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int blk = i * S::kWaves + wave, r = blk * (1024 / kRB) + lrow;
-      const int64_t off = row_at[g * kKeys + r] + ((lslot ^ S::swizzle(r)) << 4);
-      __builtin_amdgcn_global_load_lds((const void*)(c.k + off), (lds_void_t*)(stage + blk * 1024), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const void*)(c.v + off), (lds_void_t*)(stage + S::kTile + blk * 1024), 16, 0, 0);
+      const int64_t at = row_at[g * kKeys + r];
+      __builtin_amdgcn_global_load_lds((const void*)(c.k + at + ((lslot ^ S::k_swizzle(r)) << 4)),
+                                       (lds_void_t*)(stage + blk * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(c.v + at + ((lslot ^ S::v_swizzle(r)) << 4)),
+                                       (lds_void_t*)(stage + S::kTile + blk * 1024), 16, 0, 0);
     }
     e0 = e1;
     e1 = e2;
@@ -823,10 +902,26 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   wait_vm<0>();
 }
 
-// Joins the pieces of cut items.  The workgroups of an item's pieces share its
-// rows: 256 threads take as many groups of pieces as there are (up to 16) of
-// 256 / groups vectors of the result, and the groups' sums are added in their
-// order, so nothing depends on which piece finished first.
+// Joins the pieces of cut items, in the order of the line: nothing depends on
+// which piece finished first.  kJoinWgs workgroups for each piece share the
+// rows of its items.  Up to 8 pieces, a thread adds the parts of its 4
+// elements; with more, 16 threads do, and their sums are added in their order.
+constexpr int kJoinWgs = 4;
+
+struct JoinSum {
+  float top = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(float m2, float l2, const float (&p)[4]) {
+    const float next = fmaxf(top, m2);
+    // a part that saw nothing has l = 0, or NaN for a bad page, and O = 0
+    const float w1 = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(top - next);
+    const float w2 = m2 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m2 - next);
+    top = next;
+    l = l * w1 + l2 * w2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = o[i] * w1 + p[i] * w2;
+  }
+};
+
 template <int DT, int D, int RW>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, FastDiv per_group) {
   using S = Shape<DT, D, RW>;
@@ -837,49 +932,42 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, FastDiv per_
   for (int slot = 0; slot < 2; ++slot) {
     const JoinItem it = joins[blockIdx.x * 2 + slot];
     if (it.n == 0) continue;
-    const int groups = it.n > 8 ? 16 : it.n > 4 ? 8 : it.n > 2 ? 4 : 2, vecs = 256 / groups;
-    const int mine = tid / vecs, total = it.rows * (D / 4);
-    for (int v0 = ((int)blockIdx.x - it.piece) * vecs; v0 < total; v0 += it.n * vecs) {
+    const int total = it.rows * (D / 4), wg = ((int)blockIdx.x - it.piece) * kJoinWgs + (int)blockIdx.y;
+    const bool few = it.n <= 8;
+    const int groups = few ? 1 : 16, vecs = 256 / groups, mine = tid / vecs;
+    for (int v0 = wg * vecs; v0 < total; v0 += it.n * kJoinWgs * vecs) {
       const int e = min(v0 + tid % vecs, total - 1), row = e / (D / 4), d = (e % (D / 4)) * 4;
-      float top = -INFINITY, l = 0.f, odd = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-      auto add = [&](float m2, float l2, float a0, float a1, float a2, float a3) {
-        const float next = fmaxf(top, m2);
-        // a part that saw nothing has l = 0, or NaN for a bad page, and O = 0
-        const float w1 = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(top - next);
-        const float w2 = m2 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m2 - next);
-        top = next;
-        l = l * w1 + l2 * w2;
-        o0 = o0 * w1 + a0 * w2;
-        o1 = o1 * w1 + a1 * w2;
-        o2 = o2 * w1 + a2 * w2;
-        o3 = o3 * w1 + a3 * w2;
-      };
+      JoinSum s;
+      float odd = 0.f;
 #pragma unroll 4
       for (int x = mine; x < it.n; x += groups) {
         const float* p = parts + ((int64_t)(it.piece + x) * 2 + (x == 0 ? 1 : 0)) * S::kPartFloats;
         const float2 ml = *reinterpret_cast<const float2*>(p + S::kRows * D + 2 * row);
         const float4 f = *reinterpret_cast<const float4*>(p + row * D + d);
         odd += p[S::kPartOdd];
-        add(ml.x, ml.y, f.x, f.y, f.z, f.w);
+        s.add(ml.x, ml.y, {f.x, f.y, f.z, f.w});
       }
-      __syncthreads();
-      sh[tid][0] = top;
-      sh[tid][1] = l;
-      sh[tid][2] = o0;
-      sh[tid][3] = o1;
-      sh[tid][4] = o2;
-      sh[tid][5] = o3;
-      sh[tid][6] = odd;
-      __syncthreads();
+      if (!few) {
+        __syncthreads();
+        sh[tid][0] = s.top;
+        sh[tid][1] = s.l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sh[tid][2 + i] = s.o[i];
+        sh[tid][6] = odd;
+        __syncthreads();
+        if (mine == 0) {
+#pragma unroll
+          for (int x = 1; x < 16; ++x) {
+            const float(&f)[7] = sh[x * vecs + tid];
+            odd += f[6];
+            s.add(f[0], f[1], {f[2], f[3], f[4], f[5]});
+          }
+        }
+      }
       if (mine != 0 || v0 + tid >= total) continue;
-      for (int x = 1; x < groups; ++x) {
-        const float(&f)[7] = sh[x * vecs + tid];
-        odd += f[6];
-        add(f[0], f[1], f[2], f[3], f[4], f[5]);
-      }
       const int flat = it.tile * S::kRows + row, node = per_group.div(flat), gh = flat - node * group;
-      const float inv = sees_any(a, it.first, it.nodes, it.start, node) ? 1.f / l : 0.f;
-      float f[4] = {o0 * inv, o1 * inv, o2 * inv, o3 * inv};
+      const float inv = sees_any(a, it.first, it.nodes, it.start, node) ? 1.f / s.l : 0.f;
+      float f[4] = {s.o[0] * inv, s.o[1] * inv, s.o[2] * inv, s.o[3] * inv};
       if constexpr (DT != DFLASH_I8) {
         if (odd != 0.f) add_odd<DT, D>(a, it.first, it.nodes, it.start, it.req, it.head, node, d, f);
       }
@@ -905,7 +993,7 @@ struct Launch {
     tree_attention_kernel<DT, D, RW><<<grid(), S::kThreads, S::kLds, s>>>(a, per_group);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    tree_join_kernel<DT, D, RW><<<grid(), 256, 0, s>>>(a, per_group);
+    tree_join_kernel<DT, D, RW><<<dim3(grid(), kJoinWgs), 256, 0, s>>>(a, per_group);
     return hipGetLastError();
   }
 };
