@@ -43,9 +43,9 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 template <int DT, int D, int RW>
 struct Shape {
   static constexpr int kRowBytes = D * (DT == DFLASH_BF16 ? 2 : 1);
-  static constexpr int kKeyWaves = kRowBytes == 512 ? (RW == 1 ? 2 : 1) : 4 / RW;
+  static constexpr int kKeyWaves = kRowBytes == 512 ? (RW == 1 ? 2 : 1) : RW == 8 ? 1 : 4 / RW;
   static constexpr int kKeys = kRowBytes == 512 ? (RW == 1 ? 64 : 32)      // keys of a step
-                               : RW == 1        ? 128
+                               : RW == 1 || RW == 8 ? 128
                                : RW == 2        ? (DT == DFLASH_BF16 && D == 128 ? 64 : 128)
                                                 : 64;
   static constexpr int kRows = 32 * RW;
@@ -59,7 +59,7 @@ struct Shape {
   static constexpr int kBadAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 16 * kKeys);   // [4 steps][2] a row without a page
   static constexpr int kStatsAt = kBadAt + 32;                             // [kKeyWaves][kRows] m, l
   static constexpr int kLds = kStatsAt + 8 * kKeyWaves * kRows;
-  static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;                 // workgroups of a CU
+  static constexpr int kPerCu = RW < 8 && kLds <= 80 * 1024 ? 2 : 1;                // workgroups of a CU
   static constexpr int kPartOdd = kRows * (D + 2);                         // a partial: O [kRows][D], m and l of each
   static constexpr int kPartFloats = kPartOdd + 4;                         // row, whether odd values were left out
   static_assert(kSubs >= 1 && kSubs <= 4 && kLoads >= 1 && kTile % (1024 * kWaves) == 0, "a step splits over the waves");
@@ -136,102 +136,17 @@ __device__ __forceinline__ bf16x8_t codes_to_bf16(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const unsigned char*)p;
-}
-
-// Transposed reads of V at LDS addresses a[i] + O0 + j STEP: among 16 lanes,
-// lane i gets column i of the 16 x 16-bit by 4-row (8-bit: 8-row) block whose
-// pieces of 8 bytes the lanes address.  One block of assembly with its own
-// wait: the compiler takes the builtins to depend on every direct load in
-// flight and would wait for the next step's.
-template <bool WIDE, int O0, int STEP>
-__device__ __forceinline__ void read_transposed(const uint32_t (&a)[4], i32x2_t (&r)[4][4]) {
-  if constexpr (WIDE)
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %16 offset:%20\n\t" "ds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
-        "ds_read_b64_tr_b16 %2, %16 offset:%22\n\t" "ds_read_b64_tr_b16 %3, %16 offset:%23\n\t"
-        "ds_read_b64_tr_b16 %4, %17 offset:%20\n\t" "ds_read_b64_tr_b16 %5, %17 offset:%21\n\t"
-        "ds_read_b64_tr_b16 %6, %17 offset:%22\n\t" "ds_read_b64_tr_b16 %7, %17 offset:%23\n\t"
-        "ds_read_b64_tr_b16 %8, %18 offset:%20\n\t" "ds_read_b64_tr_b16 %9, %18 offset:%21\n\t"
-        "ds_read_b64_tr_b16 %10, %18 offset:%22\n\t" "ds_read_b64_tr_b16 %11, %18 offset:%23\n\t"
-        "ds_read_b64_tr_b16 %12, %19 offset:%20\n\t" "ds_read_b64_tr_b16 %13, %19 offset:%21\n\t"
-        "ds_read_b64_tr_b16 %14, %19 offset:%22\n\t" "ds_read_b64_tr_b16 %15, %19 offset:%23\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[2][2]), "=&v"(r[2][3]), "=&v"(r[3][0]), "=&v"(r[3][1]), "=&v"(r[3][2]), "=&v"(r[3][3])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
+// A transposed read of V: among 16 lanes, lane i gets column i of the 16 x
+// 16-bit by 4-row (8-bit: 8-row) block whose pieces of 8 bytes the lanes
+// address.  The parameter is restrict so that the compiler tells the read from
+// the direct loads in flight (into the other stage), and does not wait for them.
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+template <int DT>
+__device__ __forceinline__ i32x2_t read_transposed(const __attribute__((address_space(3))) unsigned char* __restrict__ p) {
+  if constexpr (DT == DFLASH_BF16)
+    return __builtin_bit_cast(i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)p));
   else
-    asm volatile(
-        "ds_read_b64_tr_b8 %0, %16 offset:%20\n\t" "ds_read_b64_tr_b8 %1, %16 offset:%21\n\t"
-        "ds_read_b64_tr_b8 %2, %16 offset:%22\n\t" "ds_read_b64_tr_b8 %3, %16 offset:%23\n\t"
-        "ds_read_b64_tr_b8 %4, %17 offset:%20\n\t" "ds_read_b64_tr_b8 %5, %17 offset:%21\n\t"
-        "ds_read_b64_tr_b8 %6, %17 offset:%22\n\t" "ds_read_b64_tr_b8 %7, %17 offset:%23\n\t"
-        "ds_read_b64_tr_b8 %8, %18 offset:%20\n\t" "ds_read_b64_tr_b8 %9, %18 offset:%21\n\t"
-        "ds_read_b64_tr_b8 %10, %18 offset:%22\n\t" "ds_read_b64_tr_b8 %11, %18 offset:%23\n\t"
-        "ds_read_b64_tr_b8 %12, %19 offset:%20\n\t" "ds_read_b64_tr_b8 %13, %19 offset:%21\n\t"
-        "ds_read_b64_tr_b8 %14, %19 offset:%22\n\t" "ds_read_b64_tr_b8 %15, %19 offset:%23\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[2][2]), "=&v"(r[2][3]), "=&v"(r[3][0]), "=&v"(r[3][1]), "=&v"(r[3][2]), "=&v"(r[3][3])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
-}
-template <bool WIDE, int O0, int STEP>
-__device__ __forceinline__ void read_transposed(const uint32_t (&a)[4], i32x2_t (&r)[4][2]) {
-  if constexpr (WIDE)
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t" "ds_read_b64_tr_b16 %1, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %2, %9 offset:%12\n\t" "ds_read_b64_tr_b16 %3, %9 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %4, %10 offset:%12\n\t" "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %6, %11 offset:%12\n\t" "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[3][0]), "=&v"(r[3][1])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP));
-  else
-    asm volatile(
-        "ds_read_b64_tr_b8 %0, %8 offset:%12\n\t" "ds_read_b64_tr_b8 %1, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %2, %9 offset:%12\n\t" "ds_read_b64_tr_b8 %3, %9 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %4, %10 offset:%12\n\t" "ds_read_b64_tr_b8 %5, %10 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %6, %11 offset:%12\n\t" "ds_read_b64_tr_b8 %7, %11 offset:%13\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[3][0]), "=&v"(r[3][1])
-        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O0 + STEP));
-}
-template <bool WIDE, int O0, int STEP>
-__device__ __forceinline__ void read_transposed(const uint32_t (&a)[2], i32x2_t (&r)[2][4]) {
-  if constexpr (WIDE)
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %8 offset:%10\n\t" "ds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
-        "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t" "ds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b16 %4, %9 offset:%10\n\t" "ds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
-        "ds_read_b64_tr_b16 %6, %9 offset:%12\n\t" "ds_read_b64_tr_b16 %7, %9 offset:%13\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3])
-        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
-  else
-    asm volatile(
-        "ds_read_b64_tr_b8 %0, %8 offset:%10\n\t" "ds_read_b64_tr_b8 %1, %8 offset:%11\n\t"
-        "ds_read_b64_tr_b8 %2, %8 offset:%12\n\t" "ds_read_b64_tr_b8 %3, %8 offset:%13\n\t"
-        "ds_read_b64_tr_b8 %4, %9 offset:%10\n\t" "ds_read_b64_tr_b8 %5, %9 offset:%11\n\t"
-        "ds_read_b64_tr_b8 %6, %9 offset:%12\n\t" "ds_read_b64_tr_b8 %7, %9 offset:%13\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]), "=&v"(r[1][2]), "=&v"(r[1][3])
-        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP), "n"(O0 + 2 * STEP), "n"(O0 + 3 * STEP));
-}
-template <bool WIDE, int O0, int STEP>
-__device__ __forceinline__ void read_transposed(const uint32_t (&a)[2], i32x2_t (&r)[2][2]) {
-  if constexpr (WIDE)
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %4 offset:%6\n\t" "ds_read_b64_tr_b16 %1, %4 offset:%7\n\t"
-        "ds_read_b64_tr_b16 %2, %5 offset:%6\n\t" "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
-        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP));
-  else
-    asm volatile(
-        "ds_read_b64_tr_b8 %0, %4 offset:%6\n\t" "ds_read_b64_tr_b8 %1, %4 offset:%7\n\t"
-        "ds_read_b64_tr_b8 %2, %5 offset:%6\n\t" "ds_read_b64_tr_b8 %3, %5 offset:%7\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[1][0]), "=&v"(r[1][1])
-        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O0 + STEP));
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t*)p);
 }
 
 // Sets the elements of w that are not finite to zero; whether there were any.
@@ -580,7 +495,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   auto products = [&](const unsigned char* stage, int g, int p0, bool masked) {
     const int kb0 = kw * S::kSubs * 32;             // first key of this wave
     const unsigned char* krow = stage + (kb0 + l32) * kRB;
-    const uint32_t v0 = lds_address(stage + S::kTile + kb0 * kRB) + vbase;
+    const auto* v0 = (const __attribute__((address_space(3))) unsigned char*)(stage + S::kTile + kb0 * kRB) + vbase;
     u32x4 kf[kRB / 32];
     auto read_keys = [&](int sub) {
 #pragma unroll
@@ -659,17 +574,13 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
       // V of up to four blocks of 32 columns: [column block][16-key operand]
       constexpr int kGroup = kBlocks < 4 ? kBlocks : 4, kPieces = DT == DFLASH_BF16 ? 4 : 2;
       i32x2_t r[kGroup][kPieces];
-      auto read_v = [&](int b, auto sub_c) {
-        uint32_t at[kGroup];
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) at[i] = v0 + (uint32_t)(((kPerBlock * (b + i)) ^ vx) << 4);
-        read_transposed<DT == DFLASH_BF16, decltype(sub_c)::value * 32 * kRB, (DT == DFLASH_BF16 ? 8 : 16) * kRB>(at, r);
-      };
       auto read_group = [&](int b) {
-        if (sub == 0) read_v(b, std::integral_constant<int, 0>());
-        else if (sub == 1) read_v(b, std::integral_constant<int, 1>());
-        else if (sub == 2) read_v(b, std::integral_constant<int, 2>());
-        else read_v(b, std::integral_constant<int, 3>());
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int x = 0; x < kPieces; ++x)
+            r[i][x] = read_transposed<DT>(v0 + (((kPerBlock * (b + i)) ^ vx) << 4) +
+                                          (sub * 32 + x * (DT == DFLASH_BF16 ? 8 : 16)) * kRB);
       };
       read_group(0);
       __builtin_amdgcn_sched_barrier(0);
@@ -777,7 +688,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
           step_barrier();
         }
       }
-      products(stage, g, p0, masked);
+      if (rw * 32 < rows) products(stage, g, p0, masked);
       ends = ++w.t == w.t1;
     }
     step_barrier();                                 // every wave is done with this stage; the addresses are there
@@ -977,10 +888,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, FastDiv per_
   }
 }
 
-// Row waves: 32 rows a wave up to 128 rows a workgroup.
-int row_waves(int32_t max_nodes, int32_t group) {
+int row_waves(const KvView& c, int32_t max_nodes, int32_t group) {
   const int64_t rows = (int64_t)max_nodes * group;
-  return rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+  if (rows <= 64) return rows <= 32 ? 1 : 2;
+  return c.head_dim < 256 && (rows + 127) / 128 % 2 == 0 ? 8 : 4;
 }
 
 template <int DT, int D, int RW>
@@ -1003,6 +914,9 @@ template <int DT, int D, class F>
 auto with_rows(int rw, const F& f) {
   if (rw == 1) return f(Launch<DT, D, 1>{});
   if (rw == 2) return f(Launch<DT, D, 2>{});
+  if constexpr (D < 256) {
+    if (rw == 8) return f(Launch<DT, D, 8>{});
+  }
   return f(Launch<DT, D, 4>{});
 }
 template <int DT, class F>
@@ -1021,11 +935,11 @@ auto with_shape(const KvView& c, int rw, const F& f) {
 }  // namespace
 
 size_t tree_attention_bytes(const KvView& c, int32_t n_req, int32_t max_nodes, int32_t n_q_heads) {
-  return with_shape(c, row_waves(max_nodes, n_q_heads / c.n_kv_heads), [](auto l) { return decltype(l)::bytes(); });
+  return with_shape(c, row_waves(c, max_nodes, n_q_heads / c.n_kv_heads), [](auto l) { return decltype(l)::bytes(); });
 }
 
 hipError_t launch_tree_attention(const TreeArgs& a, hipStream_t stream) {
-  return with_shape(a.c, row_waves(a.max_nodes, a.n_q_heads / a.c.n_kv_heads),
+  return with_shape(a.c, row_waves(a.c, a.max_nodes, a.n_q_heads / a.c.n_kv_heads),
                     [&](auto l) { return decltype(l)::run(a, stream); });
 }
 
