@@ -59,7 +59,7 @@ struct Shape {
   static constexpr int kBadAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 16 * kKeys);   // [4 steps][2] a row without a page
   static constexpr int kStatsAt = kBadAt + 32;                             // [kKeyWaves][kRows] m, l
   static constexpr int kLds = kStatsAt + 8 * kKeyWaves * kRows;
-  static constexpr int kPerCu = RW < 8 && kLds <= 80 * 1024 ? 2 : 1;                // workgroups of a CU
+  static constexpr int kPerCu = RW < 8 && kLds <= 80 * 1024 ? 2 : 1;      // workgroups of a CU
   static constexpr int kPartOdd = kRows * (D + 2);                         // a partial: O [kRows][D], m and l of each
   static constexpr int kPartFloats = kPartOdd + 4;                         // row, whether odd values were left out
   static_assert(kSubs >= 1 && kSubs <= 4 && kLoads >= 1 && kTile % (1024 * kWaves) == 0, "a step splits over the waves");
@@ -429,9 +429,9 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   const int vr = DT == DFLASH_BF16 ? 4 * half + vj : 8 * (vj >> 2) + 4 * half + (vj & 3);
   const int vx = (DT == DFLASH_BF16 ? 2 * (g16 & 1) + ((i16 >> 1) & 1) : g16 & 1) ^ S::v_swizzle(vr);
   const int vbase = vr * kRB + (i16 & 1) * 8;
-  // direct loads: lane's row of a 1 KB block, and its chunk's place in the row
-  // (the swizzle of a row repeats from block to block of a wave or is taken per load)
-  const int lrow = lane / S::kChunks, lslot = lane % S::kChunks;
+  // direct loads: this lane's row in the first of its wave's blocks of 1 KB, and its chunk's place in the row
+  const int lane_row = wave * (1024 / kRB) + lane / S::kChunks, lslot = lane % S::kChunks;
+  const int64_t* lane_rows = row_at + lane_row;
 
   // The step being looked up, two or three ahead of the products.
   Cursor<S> feed;
@@ -470,6 +470,13 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
     return true;
   };
 
+  // With more than 256 registers the accumulators lie in AGPRs, which only the
+  // matrix cores compute with.  Without this, at either end of the rare
+  // rescaling, the compiler moves them to VGPRs and back in every step (8 x 64
+  // nodes x 64 heads of 256 over 8192, bf16: 567 us, with it 479).
+  auto in_accumulators = [](f32x16_t& x) {
+    if constexpr (D == 256) asm volatile("" : "+a"(x));
+  };
   f32x16_t o[kBlocks];
   float m, l;                                      // of this lane's row; l over this lane's keys only
   bool bad, odd;                                   // a position without a page; a node's value that is not finite
@@ -565,9 +572,13 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
         m = next;
         l *= keep;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+        for (int b = 0; b < kBlocks; ++b) {
+          in_accumulators(o[b]);
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+          in_accumulators(o[b]);
+          if (D == 256) __builtin_amdgcn_sched_barrier(0);   // a block at a time: few registers
+        }
       }
       const float base = m == -INFINITY ? 0.f : m * cs;
       if (sub + 1 < S::kSubs) read_keys(sub + 1);
@@ -796,14 +807,18 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
     // a stage that nothing reads any more): at the loop's top, on every path,
     // all but these are older than the count waited for, and the compiler adds
     // no waits of its own at the other loads' uses.
+    constexpr int kStride = S::kWaves * (1024 / kRB);     // rows between a lane's; swizzles repeat after 16
+    int64_t rows_at[S::kLoads];
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) rows_at[i] = lane_rows[g * kKeys + i * kStride];
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
-      const int blk = i * S::kWaves + wave, r = blk * (1024 / kRB) + lrow;
-      const int64_t at = row_at[g * kKeys + r];
-      __builtin_amdgcn_global_load_lds((const void*)(c.k + at + ((lslot ^ S::k_swizzle(r)) << 4)),
-                                       (lds_void_t*)(stage + blk * 1024), 16, 0, 0);
+      const int64_t at = rows_at[i];
+      const int r = lane_row + i * kStride % 16;
+      unsigned char* to = stage + wave * 1024 + i * S::kWaves * 1024;
+      __builtin_amdgcn_global_load_lds((const void*)(c.k + at + ((lslot ^ S::k_swizzle(r)) << 4)), (lds_void_t*)to, 16, 0, 0);
       __builtin_amdgcn_global_load_lds((const void*)(c.v + at + ((lslot ^ S::v_swizzle(r)) << 4)),
-                                       (lds_void_t*)(stage + S::kTile + blk * 1024), 16, 0, 0);
+                                       (lds_void_t*)(to + S::kTile), 16, 0, 0);
     }
     e0 = e1;
     e1 = e2;
