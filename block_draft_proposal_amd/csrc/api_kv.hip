@@ -13,6 +13,11 @@ using namespace dflash;
 
 constexpr int kMaxGroup = 64, kMaxNodes = 4096;
 
+// The largest extent of a tensor in bytes: offsets in it stay far from 2^63.
+constexpr int64_t kMaxExtent = (int64_t)1 << 60;
+// The largest grid dimension in threads.
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 256;
+
 int64_t code_bytes(int32_t dtype) { return dtype == DFLASH_BF16 ? 2 : 1; }
 
 // Checks a cache and fills the view's side of it.
@@ -32,6 +37,8 @@ int view_cache(const dflash_kv_cache* c, KvView& v, const char* who) {
   if (c->page_stride < rows * c->head_dim || c->page_stride > ((int64_t)1 << 40))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: page_stride outside n_kv_heads * page_size * head_dim .. 2^40", who);
   if (c->page_stride * size % 16) return fail(DFLASH_ERR_INVALID_ARG, "%s: page_stride must be a multiple of 16 bytes", who);
+  if (c->page_stride > kMaxExtent / size / c->n_pages)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache is beyond 2^60 bytes", who);
   if (!c->k || !c->v) return fail(DFLASH_ERR_INVALID_ARG, "%s: null cache pointer", who);
   if (!aligned16(c->k) || !aligned16(c->v))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache must be 16-byte aligned", who);
@@ -40,6 +47,8 @@ int view_cache(const dflash_kv_cache* c, KvView& v, const char* who) {
     return fail(DFLASH_ERR_INVALID_ARG, "%s: scales belong to the 8-bit caches, and both to those", who);
   if (scaled && (c->scale_page_stride < rows || c->scale_page_stride > ((int64_t)1 << 40)))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: scale_page_stride outside n_kv_heads * page_size .. 2^40", who);
+  if (scaled && c->scale_page_stride > kMaxExtent / c->n_pages)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the scales are beyond 2^60 bytes", who);
   v = KvView{};
   v.k = static_cast<unsigned char*>(c->k);
   v.v = static_cast<unsigned char*>(c->v);
@@ -100,7 +109,16 @@ int check_rows(const void* p, int64_t row, int64_t head, int64_t n_rows, int32_t
   const int64_t limit = (int64_t)1 << 40;
   if (head < 0 || row < 0 || row > limit || head > limit)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: strides of %s must be in 0 .. 2^40", who, name);
+  if (row > kMaxExtent / size / 2 / n_rows || head > kMaxExtent / size / 4 / heads)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: %s is beyond 2^60 bytes", who, name);
   bytes = (size_t)(((n_rows - 1) * row + (heads - 1) * head + dim) * size);
+  return DFLASH_OK;
+}
+
+// A thread holds 8 elements of a row in the write and the read.
+int check_stream(const KvView& v, const char* who) {
+  if (v.n_rows > kMaxThreads / (v.head_dim / 8))
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_rows * head_dim must be below 2^35", who);
   return DFLASH_OK;
 }
 
@@ -123,6 +141,7 @@ int dflash_kv_write(const dflash_kv_cache* cache, const dflash_kv_batch* batch, 
   if ((st = view_batch(batch, true, c, who)) != DFLASH_OK) return st;
   if (!dtype_ok(dtype)) return fail(DFLASH_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
   if (c.n_req == 0 || c.n_rows == 0) return ok();
+  if ((st = check_stream(c, who)) != DFLASH_OK) return st;
   size_t kb = 0, vb = 0;
   if ((st = check_rows(k, k_row_stride, k_head_stride, c.n_rows, c.n_kv_heads, c.head_dim, elem_bytes(dtype), kb, "k",
                        who)) != DFLASH_OK ||
@@ -145,6 +164,7 @@ int dflash_kv_read(const dflash_kv_cache* cache, const dflash_kv_batch* batch, v
   if ((st = view_batch(batch, true, c, who)) != DFLASH_OK) return st;
   if (!dtype_ok(dtype)) return fail(DFLASH_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
   if (c.n_req == 0 || c.n_rows == 0) return ok();
+  if ((st = check_stream(c, who)) != DFLASH_OK) return st;
   if (!k_out || !v_out) return fail(DFLASH_ERR_INVALID_ARG, "%s: null output", who);
   if (!aligned16(k_out) || !aligned16(v_out))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: k_out and v_out must be 16-byte aligned", who);
@@ -165,6 +185,8 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
   if (path_width < 0 || path_stride < path_width)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: need 0 <= path_width <= path_stride", who);
   if (c.n_req == 0 || path_width == 0) return ok();
+  if ((int64_t)c.n_req * c.n_kv_heads > kMaxThreads / 128)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_req * n_kv_heads must be below 2^25", who);
   if (!paths || !path_lens) return fail(DFLASH_ERR_INVALID_ARG, "%s: null pointer", who);
   st = launch_status(launch_kv_commit(c, paths, path_stride, path_width, path_lens, as_hip(stream)), who);
   return st == DFLASH_OK ? ok() : st;
@@ -196,8 +218,8 @@ int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* b
     return fail(DFLASH_ERR_UNSUPPORTED, "%s: more than %d query heads to a kv head", who, kMaxGroup);
   if (max_nodes < 1) return fail(DFLASH_ERR_INVALID_ARG, "%s: max_nodes must be >= 1", who);
   if (max_nodes > kMaxNodes) return fail(DFLASH_ERR_UNSUPPORTED, "%s: max_nodes > %d", who, kMaxNodes);
-  if (!std::isfinite(scale) || scale <= 0.f)
-    return fail(DFLASH_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+  if (!std::isfinite(scale) || scale <= 0.f || scale > 0x1p100f)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: scale must be > 0 and at most 2^100", who);
   if (mask ? mask_words < (max_nodes + 63) / 64 : mask_words != 0)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: mask_words must be >= ceil(max_nodes / 64) with a mask, 0 without", who);
   if (reinterpret_cast<uintptr_t>(mask) & 7) return fail(DFLASH_ERR_INVALID_ARG, "%s: mask must be 8-byte aligned", who);
@@ -214,6 +236,8 @@ int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* b
     return fail(DFLASH_ERR_WORKSPACE, "%s: workspace of %zu bytes < %zu needed", who, workspace_bytes, need);
   if (need && (reinterpret_cast<uintptr_t>(workspace) & 255))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  if (overlaps(workspace, need, out, ob) || overlaps(workspace, need, q, qb) || meets_cache(a.c, workspace, need))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the workspace overlaps q, out or the cache", who);
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_row_stride;
   a.q_head = q_head_stride;

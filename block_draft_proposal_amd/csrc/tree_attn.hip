@@ -86,7 +86,8 @@ struct Shape {
 constexpr int kItemCost = 2;
 // A piece is at least this long: below, the join costs more than the split saves.
 constexpr int kMinPiece = 4;
-// Lengths beyond this have no positions (their rows are NaN).
+// Lengths beyond this, or beyond the page table, have no positions: such a
+// request takes one step, whatever its length claims to be, and is NaN.
 constexpr int kMaxLen = 0x7fffffff - (1 << 17);
 
 template <int N>
@@ -179,10 +180,10 @@ struct Req {
   int32_t first;             // its first row
   int32_t n;                 // nodes
   int32_t start;             // prefix positions
-  int32_t len;               // start + n, at most kMaxLen
+  int32_t len;               // start + n; 1 where over
   int32_t steps;             // ceil(len / keys); 0 without nodes
   int32_t tiles;             // row tiles
-  bool over;                 // start + n is beyond kMaxLen
+  bool over;                 // start + n is beyond kMaxLen or the table
   __device__ __forceinline__ int64_t cost(int heads) const {
     return steps ? (int64_t)(steps + kItemCost) * (tiles * heads) : 0;
   }
@@ -194,8 +195,8 @@ __device__ __forceinline__ Req make_request(const TreeArgs& a, int32_t first, in
   q.first = first;
   q.n = (int32_t)n;
   q.start = max(start, 0);
-  q.over = q.start + n > kMaxLen;
-  q.len = (int32_t)min(q.start + n, (int64_t)kMaxLen);
+  q.over = q.start + n > min((int64_t)kMaxLen, (int64_t)a.c.table_width * a.c.page_size);
+  q.len = q.over ? 1 : (int32_t)(q.start + n);
   q.steps = n > 0 ? (q.len + KEYS - 1) / KEYS : 0;
   q.tiles = (q.n * group + ROWS - 1) / ROWS;
   return q;

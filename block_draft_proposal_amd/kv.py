@@ -5,6 +5,7 @@ Functions have the names of the C entry points, take torch tensors on one GPU
 and enqueue on the current stream of that GPU (or on ``stream``)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -160,6 +161,12 @@ def _call(fn, cache: KVCache, stream, *args) -> None:
     _b._check(status)
 
 
+def _on(stream):
+    """New tensors belong to the stream that uses them: the allocator then
+    gives their memory to no other stream's work while it is in use."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def dflash_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, *, page_table: torch.Tensor,
                     start: torch.Tensor, offsets: torch.Tensor, stream=None) -> None:
     """Stores k, v [n_rows, n_kv_heads, head_dim] (bf16 or fp32, strided views
@@ -185,8 +192,9 @@ def dflash_kv_read(cache: KVCache, *, page_table: torch.Tensor, start: torch.Ten
         if n_rows is None:
             raise ValueError("n_rows is needed without k_out and v_out")
         shape = (n_rows, cache.n_kv_heads, cache.head_dim)
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device) if v_out is None else v_out
+        with _on(stream):
+            k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.device) if v_out is None else v_out
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         _rows(t, name, cache, cache.n_kv_heads)
         if not t.is_contiguous():
@@ -238,13 +246,15 @@ def dflash_tree_attention(q: torch.Tensor, cache: KVCache, *, page_table: torch.
             raise ValueError("mask must be contiguous int64 [n_rows, words] on the cache's GPU")
         words = mask.shape[1]
     if out is None:
-        out = torch.empty((n_rows, n_q_heads, head_dim), dtype=torch.bfloat16, device=cache.device)
+        with _on(stream):
+            out = torch.empty((n_rows, n_q_heads, head_dim), dtype=torch.bfloat16, device=cache.device)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != cache.device:
         raise ValueError("out must be contiguous bf16 of q's shape on the cache's GPU")
     fns = _fns()
     if workspace is None:
         nbytes = fns.dflash_tree_attention_workspace_size(cache.ref, batch.n_req, max_nodes, n_q_heads)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device)
+        with _on(stream):
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.device)
     elif workspace.device != cache.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's GPU")
     _call(fns.dflash_tree_attention, cache, stream, cache.ref, ctypes.byref(batch), q.data_ptr(), *_strides(q),

@@ -29,7 +29,8 @@
  * Page tables, lengths and offsets are device data and cannot be checked on
  * the host.  A position whose page index lies outside the table's width, or
  * whose page lies outside [0, n_pages), touches no memory: it is not written,
- * reads as NaN, and makes the attention rows of its request NaN.
+ * reads as NaN, and makes the attention rows of its request NaN (but for rows
+ * that see nothing, which are zeros).  So do lengths beyond 2^31 - 2^17.
  */
 #ifndef DFLASH_KV_H
 #define DFLASH_KV_H
@@ -82,10 +83,13 @@ typedef struct {
  *     code = x * 2^-e rounded once (nearest, ties to even).
  *     A row that holds an infinity or a NaN gets scale byte 255 and codes 0,
  *     so that it reads back as NaN.
+ *     Above 2^127 a row's largest values may round to a code that reads back
+ *     beyond the range, as an infinity.
  *   k, v  row i, kv head h at k + i * k_row_stride + h * k_head_stride (strides
  *         in elements), head_dim contiguous elements of `dtype` (DFLASH_BF16
  *         or DFLASH_F32); pointers and strides multiples of 16 bytes; they may
  *         not overlap the cache.
+ * n_rows * head_dim is below 2^35 (here and in dflash_kv_read).
  * Positions written by one call must be distinct rows of the cache: requests
  * may share pages that they only read, not pages that they write. */
 int dflash_kv_write(const dflash_kv_cache* cache, const dflash_kv_batch* batch, const void* k, int64_t k_row_stride,
@@ -113,7 +117,8 @@ int dflash_kv_read(const dflash_kv_cache* cache, const dflash_kv_batch* batch, v
  *   paths      row r at paths + r * path_stride, path_width entries
  *   path_lens  [n_req]; lengths beyond path_width count as path_width
  * Only page_table, table_stride, table_width, start and n_req of the batch
- * are used.  Pages moved by one call may not be shared between requests. */
+ * are used; n_req * n_kv_heads is below 2^25.  Pages moved by one call may not
+ * be shared between requests. */
 int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch, const int32_t* paths,
                      int64_t path_stride, int32_t path_width, const int32_t* path_lens, dflash_stream_t stream);
 
@@ -136,12 +141,18 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
  *         not overlap q or the cache
  *   max_nodes  1 .. 4096: no request has more nodes (rows of a request beyond
  *         it are left as they were)
- *   scale finite and > 0
+ *   scale > 0, at most 2^100
  * n_q_heads is a multiple of n_kv_heads, up to 64 query heads to a kv head.
  * Arithmetic: products exact in fp32, sums, maximum and softmax in fp32; the
  * weights are rounded to bf16 for the product with V, the result once to bf16.
+ * The sums keep weights up to 2^8, so |v| * positions has to stay below 2^119:
+ * beyond, a result may be an infinity.  A call's result is the same every
+ * time; its sums are split by the lengths of the whole batch, so a request
+ * may differ in the last bits from one batch to another.
  * Scratch: dflash_tree_attention_workspace_size() bytes, 256-byte aligned; it
- * does not depend on the lengths, so one workspace serves a growing cache. */
+ * does not depend on the lengths, so one workspace serves a growing cache.
+ * It may not overlap q, out or the cache, and calls that may run at the same
+ * time need one each. */
 size_t dflash_tree_attention_workspace_size(const dflash_kv_cache* cache, int32_t n_req, int32_t max_nodes,
                                             int32_t n_q_heads);
 int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* batch, const void* q,

@@ -135,6 +135,28 @@ def test_tree_refusals():
     assert K._fns().dflash_tree_attention_workspace_size(_structs()[0], 2, 4, 33) == 0
 
 
+def test_extents_beyond_what_offsets_hold():
+    for call in (_write, _read, _commit, _tree):
+        assert call(cache=dict(page_stride=1 << 40, n_pages=1 << 30)) == -1
+        assert call(cache={**SCALED, "scale_page_stride": 1 << 40, "n_pages": (1 << 31) - 1}) == -1
+    assert _write(batch=dict(n_rows=(1 << 31) - 1), kr=1 << 30) == -2
+    assert _write(batch=dict(n_rows=1 << 27), kr=1 << 40) == -1
+    assert _tree(batch=dict(n_rows=(1 << 31) - 1), qr=1 << 40) == -1
+    # grids past 2^32 threads
+    assert _write(batch=dict(n_rows=1 << 28)) == -2
+    assert _read(batch=dict(n_rows=1 << 28)) == -2
+    assert _commit(batch=dict(n_req=1 << 22)) == -2
+    assert _tree(scale=2.0 ** 101) == -1
+
+
+def test_workspace_apart_from_the_rest():
+    need = K._fns().dflash_tree_attention_workspace_size(_structs()[0], 2, 4, 32)
+    assert need > 0
+    for at in (1 << 40, 2 << 40, 8 << 40, 9 << 40):     # the cache's K and V, q, out
+        assert _tree(ws=at, ws_bytes=need) == -1, at
+    assert _tree(cache=SCALED, ws=6 << 40, ws_bytes=1 << 60) == -1
+
+
 def test_cache_object_refuses_what_is_no_cache():
     k = torch.empty((4, 2, 16, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="GPU"):

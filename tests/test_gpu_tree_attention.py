@@ -244,3 +244,113 @@ def test_offsets_beyond_32_bits():
     near = D.dflash_tree_attention(s["q"], s["cache"], **s["kw"])
     torch.cuda.synchronize()
     assert torch.equal(far[:5], near[:5])
+
+
+WIDE = [
+    # more than 128 rows to a kv head: pairs of 128-row tiles, and odd numbers of them
+    ([300, 5, 0], [64, 20, 33], 16, 1, 4, 128, "tree"),
+    ([77], [130], 20, 2, 2, 128, "random"),
+    ([40, 129], [300, 1], 16, 1, 1, 64, "random"),
+    ([1000, 10], [200, 7], 32, 1, 2, 64, "tree"),
+    ([129, 0], [16, 2], 16, 1, 64, 128, "random"),
+    ([50, 600], [30, 64], 16, 2, 8, 256, "tree"),
+    ([5, 260], [140, 100], 1, 1, 2, 128, "chain"),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: f"s{c[0][0]}n{max(c[1])}p{c[2]}h{c[3]}g{c[4]}d{c[5]}{c[6]}")
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
+def test_many_rows_to_a_kv_head(case, kind):
+    require_gpu()
+    start, rows, page, heads, group, dim, mask = case
+    say(f"tree attention {case} {kind}")
+    check(build(kind, start, rows, page, heads, group, dim, mask, seed=sum(start) % 89))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_long_context_in_many_pieces_and_room_for_many_nodes(dim):
+    """Items cut into more than eight pieces; max_nodes far above the nodes."""
+    require_gpu()
+    say(f"many pieces {dim}")
+    check(build("e4m3", [9000, 2], [5, 3], 16, 1, 4, dim, "tree", seed=8, max_nodes=4096))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [40, 64])
+@pytest.mark.parametrize("start", [20, 9000])
+def test_unseen_values_of_wide_and_cut_items(kind, nodes, start):
+    require_gpu()
+    say(f"masked values {kind} {nodes} {start}")
+    s = build(kind, [start], [nodes], 16, 1, 8, 128, "tree", seed=11)
+    clean = codes_f64(D.dflash_tree_attention(s["q"], s["cache"], **s["kw"]))
+    at = start + 5
+    v = s["cache"].v.view(torch.uint8) if kind == "e4m3" else s["cache"].v
+    v[int(s["host"][0][0, at // 16]), :, at % 16, 3::7] = 0x7F if kind == "e4m3" else float("-inf")
+    dirty = codes_f64(D.dflash_tree_attention(s["q"], s["cache"], **s["kw"]))
+    seen = np.array([bool(int(s["bits"][i, 0]) & 32) for i in range(nodes)])
+    assert 2 < seen.sum() < nodes - 2
+    np.testing.assert_array_equal(dirty[:nodes][~seen], clean[:nodes][~seen])
+    np.testing.assert_array_equal(np.isfinite(dirty[:nodes][seen][..., 3::7]), False)
+    rest = np.arange(128) % 7 != 3
+    np.testing.assert_array_equal(dirty[:nodes][seen][..., rest], clean[:nodes][seen][..., rest])
+
+
+def test_lengths_beyond_the_table_take_one_step():
+    """A length that the table does not reach (up to the largest int32) makes
+    its request NaN and leaves the others as they are."""
+    require_gpu()
+    say("lengths beyond the table")
+    s = build("i8", [50, 20, 300], [4, 4, 2], 16, 2, 4, 128, "tree", seed=4)
+    clean = codes_f64(D.dflash_tree_attention(s["q"], s["cache"], **s["kw"]))
+    width = s["host"][0].shape[1]
+    for far in (width * 16 - 3, 1 << 30, (1 << 31) - 1):
+        s["kw"]["start"] = torch.tensor([far, 20, far], dtype=torch.int32, device=DEV)
+        got = codes_f64(D.dflash_tree_attention(s["q"], s["cache"], **s["kw"]))
+        assert np.isnan(got[:4]).all()
+        assert np.isnan(got[8:10]).all() or far == width * 16 - 3
+        np.testing.assert_array_equal(got[4:8], clean[4:8])
+
+
+def test_strided_table_and_query_without_strides():
+    require_gpu()
+    say("strided table, expanded query")
+    s = build("bf16", [50, 20], [4, 6], 16, 2, 4, 128, "tree", seed=12)
+    want = D.dflash_tree_attention(s["q"], s["cache"], **s["kw"])
+    table = s["kw"]["page_table"]
+    wide = torch.full((2, table.shape[1] + 9), -1, dtype=torch.int32, device=DEV)
+    wide[:, 2:2 + table.shape[1]] = table
+    s["kw"]["page_table"] = wide[:, 2:-1]
+    got = D.dflash_tree_attention(s["q"], s["cache"], **s["kw"])
+    assert torch.equal(got[:10], want[:10])
+    one = s["q"][:1, :1].expand(s["q"].shape)
+    got = D.dflash_tree_attention(one, s["cache"], **s["kw"])
+    want = D.dflash_tree_attention(one.contiguous(), s["cache"], **s["kw"])
+    assert torch.equal(got[:10], want[:10])
+
+
+def test_no_rows_and_no_requests():
+    require_gpu()
+    say("nothing to do")
+    s = build("bf16", [50, 20], [4, 6], 16, 2, 4, 64, "chain", seed=13)
+    kw = dict(s["kw"], page_table=s["kw"]["page_table"][:0], start=s["kw"]["start"][:0], offsets=s["kw"]["offsets"][:1])
+    assert D.dflash_tree_attention(s["q"], s["cache"], **kw).shape == s["q"].shape
+    assert D.dflash_tree_attention(s["q"][:0], s["cache"], **s["kw"]).shape[0] == 0
+    torch.cuda.synchronize()
+
+
+def test_new_tensors_of_a_call_on_another_stream_are_its_own():
+    """The workspace that a call makes is given to nobody while the call's
+    stream still has to run it."""
+    require_gpu()
+    say("workspace of another stream")
+    s = build("bf16", [2500, 40], [6, 16], 16, 2, 4, 128, "tree", seed=21)
+    want = D.dflash_tree_attention(s["q"], s["cache"], **s["kw"]).clone()
+    size = D.tree_attention_workspace_size(s["cache"], n_req=2, max_nodes=16, n_q_heads=8)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = D.dflash_tree_attention(s["q"], s["cache"], stream=side, **s["kw"])
+    others = [torch.zeros(size, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[:22], want[:22]) and not any(x.any() for x in others)
