@@ -151,14 +151,21 @@ def _strides(t: torch.Tensor):
 
 def _call(fn, cache: KVCache, stream, *args) -> None:
     """fn(*args, stream handle) with the cache's GPU current."""
-    if stream is not None and stream.device != cache.device:
+    index = cache.device.index
+    if stream is None:
+        # the handle alone: 0.1 us, torch.cuda.current_stream() takes 2.6, a whole call 7
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device != cache.device:
         raise ValueError("stream belongs to another GPU than the cache")
-    if cache.device.index == torch.cuda.current_device():
-        status = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
     else:
-        with torch.cuda.device(cache.device):
-            status = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
-    _b._check(status)
+        handle = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status:
+        _b._check(status)
 
 
 def _on(stream):
