@@ -9,6 +9,12 @@
 // rows.  A thread finds its token's request, page and slot once and then
 // takes kUnits (kv head, K or V) pairs, all loads issued before the first is
 // used.
+//
+// Measured: 64 ragged prompts of up to 2048 rows, 8 heads of 128, bf16 into
+// e4m3 (403 MB read and written) 74.5 us, 5.4 TB/s; 16 contexts of up to 8192
+// back in bf16 (407 MB) 73 us, 5.6 TB/s; a copy of 2 GiB runs at 6.0.  The
+// blocks of 32 requests are written in 3.1 us and a path is committed in 3.0,
+// 256 requests' in 6: latency.
 #include "kv_cache.h"
 
 namespace dflash {
@@ -50,21 +56,31 @@ struct RowPlace {
   int32_t slot;
 };
 
-// 8 consecutive elements of a dense row as fp32.
-template <int SRC>
+// A lane's 8 elements of a row of LPR * 8: lane `part` takes 8 consecutive ones
+// of a bf16 dense row, and of an fp32 one 4 in either half, so that each of
+// its two 16-byte accesses is part of one run (int8 to fp32, 16 ragged
+// requests of up to 4096 rows x 8 heads of 128: 74 us, with 8 consecutive 121;
+// fp32 to e4m3, 64 of up to 1024: 70 us, with 8 consecutive 79).
+template <int DENSE, int LPR>
+__device__ __forceinline__ int first_of(int part) { return DENSE == DFLASH_F32 ? part * 4 : part * 8; }
+template <int DENSE, int LPR>
+__device__ __forceinline__ int second_of(int part) { return DENSE == DFLASH_F32 ? LPR * 4 + part * 4 : part * 8 + 4; }
+
+// They are loaded from a dense row and widened to fp32.
+template <int SRC, int LPR>
 struct Eight;
-template <>
-struct Eight<DFLASH_BF16> {
+template <int LPR>
+struct Eight<DFLASH_BF16, LPR> {
   u32x4 w;
-  __device__ __forceinline__ void load(const void* p, int64_t at) { w = ld16_nt((const uint16_t*)p + at); }
+  __device__ __forceinline__ void load(const void* p, int64_t at, int part) { w = ld16_nt((const uint16_t*)p + at + part * 8); }
   __device__ __forceinline__ void get(float (&x)[8]) const { unpack16(w, x); }
 };
-template <>
-struct Eight<DFLASH_F32> {
+template <int LPR>
+struct Eight<DFLASH_F32, LPR> {
   u32x4 w0, w1;
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    w0 = ld16_nt((const float*)p + at);
-    w1 = ld16_nt((const float*)p + at + 4);
+  __device__ __forceinline__ void load(const void* p, int64_t at, int part) {
+    w0 = ld16_nt((const float*)p + at + first_of<DFLASH_F32, LPR>(part));
+    w1 = ld16_nt((const float*)p + at + second_of<DFLASH_F32, LPR>(part));
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     float a[4], b[4];
@@ -77,6 +93,14 @@ struct Eight<DFLASH_F32> {
     }
   }
 };
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+// Stores to the cache; NT passes the hardware's caches by.
+template <bool NT, class T>
+__device__ __forceinline__ void put(void* p, T v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
+  else *reinterpret_cast<T*>(p) = v;
+}
 
 // LPR lanes of 8 elements hold one row.  grid.x covers the batch's rows,
 // grid.y the (kv head, K or V) pairs in groups of UNITS.
@@ -92,12 +116,18 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(KvView c, KvRows in)
   if (live) live = kv_locate(c, c.table + req * c.table_stride, pos, page, slot);
   if (!live) return;                              // whole rows: the lanes of a row leave together
   const int units = 2 * c.n_kv_heads, u0 = blockIdx.y * UNITS;
-  Eight<SRC> e[UNITS];
+  Eight<SRC, LPR> e[UNITS];
+  // Large batches are not in the caches any more when they are read.  Whole
+  // runs of 128 bytes and more pass them by (e4m3 from bf16: 74.5 us, through
+  // them 81; bf16 51 and 55), shorter ones would cost (64 int8: 23.9 and 22.4;
+  // fp32 rows' halves: 74 and 70).
+  constexpr bool kNt = UNITS > 1 && SRC == DFLASH_BF16 && (DT == DFLASH_BF16 || LPR >= 16);
+  const int first = first_of<SRC, LPR>(part), second = second_of<SRC, LPR>(part);
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
     const int u = min(u0 + i, units - 1), h = u >> 1;
-    if (u & 1) e[i].load(in.v, t * in.v_row + h * in.v_head + part * 8);
-    else e[i].load(in.k, t * in.k_row + h * in.k_head + part * 8);
+    if (u & 1) e[i].load(in.v, t * in.v_row + h * in.v_head, part);
+    else e[i].load(in.k, t * in.k_row + h * in.k_head, part);
   }
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
@@ -108,15 +138,16 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(KvView c, KvRows in)
     const int64_t row = (int64_t)h * c.page_size + slot;
     unsigned char* page_at = ((u & 1) ? c.v : c.k) + page * c.page_bytes;
     if constexpr (DT == DFLASH_BF16) {
-      u32x4 w;
       if constexpr (SRC == DFLASH_BF16) {
-        w = e[i].w;                               // no rounding: the bits as they are
+        put<kNt>(page_at + (row * (LPR * 8) + first) * 2, e[i].w);   // no rounding: the bits as they are
       } else {
+        u32x4 w;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           w[j] = f32_to_bf16_rne(x[2 * j]) | (f32_to_bf16_rne(x[2 * j + 1]) << 16);
+        put<kNt>(page_at + (row * (LPR * 8) + first) * 2, u32x2{w[0], w[1]});
+        put<kNt>(page_at + (row * (LPR * 8) + second) * 2, u32x2{w[2], w[3]});
       }
-      st16(page_at + (row * (LPR * 8) + part * 8) * 2, w);
     } else {
       // the largest magnitude by its bits, which order as the values do; an
       // infinity or NaN has the largest
@@ -149,7 +180,12 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(KvView c, KvRows in)
           hi = r[4] | (r[5] << 8) | (r[6] << 16) | (r[7] << 24);
         }
       }
-      *reinterpret_cast<uint2*>(page_at + row * (LPR * 8) + part * 8) = make_uint2(lo, hi);
+      if constexpr (SRC == DFLASH_BF16) {
+        put<kNt>(page_at + row * (LPR * 8) + first, u32x2{lo, hi});
+      } else {
+        put<kNt>(page_at + row * (LPR * 8) + first, lo);
+        put<kNt>(page_at + row * (LPR * 8) + second, hi);
+      }
       if (part == 0) ((u & 1) ? c.v_scale : c.k_scale)[page * c.scale_page_bytes + row] = (uint8_t)byte;
     }
   }
@@ -165,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvView c, void* k_out
   int64_t pos = 0, page = 0;
   if (!kv_row_position(c, t0, t, req, pos)) return;
   const bool held = kv_locate(c, c.table + req * c.table_stride, pos, page, slot);   // else page 0, slot 0 is read
+  const int first = first_of<DST, LPR>(part), second = second_of<DST, LPR>(part);
   const int units = 2 * c.n_kv_heads, u0 = blockIdx.y * UNITS;
   u32x4 w[UNITS];
   uint32_t byte[UNITS];
@@ -174,13 +211,23 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvView c, void* k_out
     const int64_t row = (int64_t)h * c.page_size + slot;
     const unsigned char* page_at = ((u & 1) ? c.v : c.k) + page * c.page_bytes;
     if constexpr (DT == DFLASH_BF16) {
-      w[i] = ld16_nt(page_at + (row * D + part * 8) * 2);
+      if constexpr (DST == DFLASH_BF16) {
+        w[i] = ld16_nt(page_at + (row * D + first) * 2);
+      } else {
+        const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(page_at + (row * D + first) * 2));
+        const u32x2 b = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(page_at + (row * D + second) * 2));
+        w[i] = u32x4{a[0], a[1], b[0], b[1]};
+      }
       byte[i] = 127;
     } else {
-      typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-      const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(page_at + row * D + part * 8));
-      w[i][0] = a[0];
-      w[i][1] = a[1];
+      if constexpr (DST == DFLASH_BF16) {
+        const u32x2 a = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(page_at + row * D + first));
+        w[i][0] = a[0];
+        w[i][1] = a[1];
+      } else {
+        w[i][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(page_at + row * D + first));
+        w[i][1] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(page_at + row * D + second));
+      }
       byte[i] = ((u & 1) ? c.v_scale : c.k_scale)[page * c.scale_page_bytes + row];
     }
   }
@@ -206,17 +253,17 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(KvView c, void* k_out
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __builtin_nanf("");
     }
-    const int64_t at = (t * c.n_kv_heads + h) * D + part * 8;
+    const int64_t at = (t * c.n_kv_heads + h) * D;
     void* out = (u & 1) ? v_out : k_out;
     if constexpr (DST == DFLASH_BF16) {
       u32x4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
       if (DT == DFLASH_BF16 && held) o = w[i];    // no arithmetic: the bits as they are
-      st16_nt((uint16_t*)out + at, o);
+      st16_nt((uint16_t*)out + at + first, o);
     } else {
-      st16_nt((float*)out + at, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])});
-      st16_nt((float*)out + at + 4, u32x4{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])});
+      st16_nt((float*)out + at + first, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])});
+      st16_nt((float*)out + at + second, u32x4{__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])});
     }
   }
 }
@@ -266,7 +313,9 @@ __global__ void __launch_bounds__(kThreads) kv_commit_kernel(KvView c, const int
 }
 
 // (kv head, K or V) pairs per thread: 4 keep enough loads in flight for the
-// stream; 1 where the batch is too small to fill the chip with 4.
+// stream (64 ragged prompts into e4m3: 75 us, with 2 93, with 1 137, with 8
+// 75; read back 73, 89, 161, 73); 1 where the batch is too small to fill the
+// chip with 4 (32 blocks of 16: 3.1 us, with 4 3.8).
 inline int units_for(int64_t n_rows, int lpr, int n_kv_heads) {
   const int64_t wgs = (n_rows * lpr + kThreads - 1) / kThreads * ((2 * n_kv_heads + 3) / 4);
   return wgs >= 1024 ? 4 : 1;

@@ -246,3 +246,36 @@ def test_capture_and_another_stream():
         for a, b in zip(captured[1], eager[1]):
             assert torch.equal(a, b)
         assert torch.equal(captured[0].k.view(torch.uint8), eager[0].k.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 9), (128, 8), (256, 5)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_large_batches_equal_small_ones(dim, heads, kind, io):
+    """Many rows at once, several (head, K or V) pairs to a thread, against the
+    same rows a few requests at a time, and K's rows against the oracle."""
+    require_gpu()
+    say(f"large batch {dim} {heads} {kind} {io}")
+    rng = np.random.default_rng(dim)
+    rows = rng.integers(0, 300, size=56)
+    (table, st, off), host, n_pages, n_rows = make_plan(rng.integers(0, 40, size=56), rows, 16, seed=3)
+    k, v = rand_rows(n_rows, heads, dim, io, 31), rand_rows(n_rows, heads, dim, io, 32)
+    large, small = (dead_cache(kind, n_pages, heads, 16, dim) for _ in range(2))
+    D.dflash_kv_write(D.KVCache(*large), k, v, page_table=table, start=st, offsets=off)
+    for r in range(0, 56, 4):
+        a, b = int(host[2][r]), int(host[2][r + 4])
+        if b > a:
+            D.dflash_kv_write(D.KVCache(*small), k[a:b], v[a:b], page_table=table[r:r + 4], start=st[r:r + 4], offsets=off[r:r + 5] - a)
+    torch.cuda.synchronize()
+    for x, y in zip(large, small):
+        assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    want = oracle_cache(*(t[:, :1] if t is not None else None for t in dead_cache(kind, n_pages, 1, 16, dim)))
+    one = [codes_f64((x.to(torch.bfloat16) if kind == "bf16" else x)[:, -1:]) for x in (k, v)]
+    O.write(want, kind, *one, *host)
+    _same(codes_f64(large[0][:, -1:]), want["k"], "k of the last head")
+    ko, vo = D.dflash_kv_read(D.KVCache(*large), page_table=table, start=st, offsets=off, n_rows=n_rows, dtype=TYPES[io])
+    ref = [np.zeros((n_rows, 1, dim)) for _ in "kv"]
+    O.read(want, *host, ref)
+    n = int(host[2][-1])
+    for o, r, name in zip((ko, vo), ref, "kv"):
+        _same(codes_f64(o[:n, -1:]), torch.from_numpy(r[:n]).to(torch.float32).to(TYPES[io]).double().numpy(), name)
