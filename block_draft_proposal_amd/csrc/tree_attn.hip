@@ -23,11 +23,25 @@
 // constant for what an item costs besides, form one line that is cut into
 // equal pieces, one for each workgroup.  A piece that covers an item writes
 // its result; pieces of a cut item leave (m, l, O) in the workspace, at most
-// two to a workgroup, and a second kernel joins them in a fixed order.
+// two to a workgroup, and a second kernel joins them in a fixed order (32
+// requests x 16 nodes, bf16: 71 us and 10).
 //
 // Loads run two steps ahead of the products and do not stop at an item's end:
 // each step's rows are looked up (page table, then addresses into LDS) by one
 // thread a row, two steps before its direct loads are issued.
+//
+// Measured (pages of 16, 8 kv heads of 128; us, both kernels): 64 requests x
+// 4 nodes x 32 heads over 8160 positions, bf16 383 (5.6 TB/s; a plain read of
+// 2 GiB runs at 6.7), e4m3 209, int8 213 (5.1): bound by HBM.  16 nodes: 396,
+// 263, 300.  8 requests x 64 nodes x 64 heads over 16384: 337, 344, 427 (820,
+// 800, 645 TFLOP/s; a library product of 8192^3 reaches 1430): a wave's chain
+// of products, exponentials and LDS reads, two waves to a SIMD, and for 8-bit
+// types the conversions.  One token over 200 positions: 14, of which a chain of
+// dependent loads (lengths, table, rows) and two launches are most.
+// Tried without gain: a ring of four stages with one barrier a step (wide
+// 330, but 16 nodes e4m3 276), two row tiles to a wave (wide 356), sums of the
+// rounded weights (wide 346, error 2.0e-3 for 2.1e-3), steps priced by their
+// rows (256 requests 502 for 484).
 #include <type_traits>
 
 #include "kv_cache.h"
@@ -59,7 +73,10 @@ struct Shape {
   static constexpr int kBadAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 16 * kKeys);   // [4 steps][2] a row without a page
   static constexpr int kStatsAt = kBadAt + 32;                             // [kKeyWaves][kRows] m, l
   static constexpr int kLds = kStatsAt + 8 * kKeyWaves * kRows;
-  static constexpr int kPerCu = RW < 8 && kLds <= 80 * 1024 ? 2 : 1;      // workgroups of a CU
+  // Workgroups of a CU, by their LDS and by registers: two waves to a SIMD,
+  // one with heads of 256 (8 x 64 nodes x 64 heads of 256 over 8192, bf16: 446
+  // us, with pieces for twice as many 480).
+  static constexpr int kPerCu = kLds <= 80 * 1024 && kWaves * (D == 256 ? 2 : 1) <= 4 ? 2 : 1;
   static constexpr int kPartOdd = kRows * (D + 2);                         // a partial: O [kRows][D], m and l of each
   static constexpr int kPartFloats = kPartOdd + 4;                         // row, whether odd values were left out
   static_assert(kSubs >= 1 && kSubs <= 4 && kLoads >= 1 && kTile % (1024 * kWaves) == 0, "a step splits over the waves");
@@ -476,7 +493,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   // With more than 256 registers the accumulators lie in AGPRs, which only the
   // matrix cores compute with.  Without this, at either end of the rare
   // rescaling, the compiler moves them to VGPRs and back in every step (8 x 64
-  // nodes x 64 heads of 256 over 8192, bf16: 567 us, with it 479).
+  // nodes x 64 heads of 256 over 8192, bf16: 567 us, with it 480).
   auto in_accumulators = [](f32x16_t& x) {
     if constexpr (D == 256) asm volatile("" : "+a"(x));
   };
