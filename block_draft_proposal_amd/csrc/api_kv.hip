@@ -122,6 +122,13 @@ int check_stream(const KvView& v, const char* who) {
   return DFLASH_OK;
 }
 
+// K and V are written side by side, in no order.
+int check_apart(const KvView& v, const char* who) {
+  if (v.k == v.v || (v.k_scale && v.k_scale == v.v_scale))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache's K and V are the same memory", who);
+  return DFLASH_OK;
+}
+
 bool tree_shape_ok(int32_t n_kv_heads, int32_t n_q_heads, int32_t max_nodes) {
   return n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 && n_q_heads / n_kv_heads <= kMaxGroup && max_nodes >= 1 &&
          max_nodes <= kMaxNodes;
@@ -142,6 +149,7 @@ int dflash_kv_write(const dflash_kv_cache* cache, const dflash_kv_batch* batch, 
   if (!dtype_ok(dtype)) return fail(DFLASH_ERR_INVALID_ARG, "%s: unknown dtype %d", who, dtype);
   if (c.n_req == 0 || c.n_rows == 0) return ok();
   if ((st = check_stream(c, who)) != DFLASH_OK) return st;
+  if ((st = check_apart(c, who)) != DFLASH_OK) return st;
   size_t kb = 0, vb = 0;
   if ((st = check_rows(k, k_row_stride, k_head_stride, c.n_rows, c.n_kv_heads, c.head_dim, elem_bytes(dtype), kb, "k",
                        who)) != DFLASH_OK ||
@@ -187,6 +195,7 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
   if (c.n_req == 0 || path_width == 0) return ok();
   if ((int64_t)c.n_req * c.n_kv_heads > kMaxThreads / 128)
     return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_req * n_kv_heads must be below 2^25", who);
+  if ((st = check_apart(c, who)) != DFLASH_OK) return st;
   if (!paths || !path_lens) return fail(DFLASH_ERR_INVALID_ARG, "%s: null pointer", who);
   st = launch_status(launch_kv_commit(c, paths, path_stride, path_width, path_lens, as_hip(stream)), who);
   return st == DFLASH_OK ? ok() : st;

@@ -106,6 +106,8 @@ def test_write_refusals():
                dict(dtype=0, kr=1022), dict(k=(1 << 40) + 256), dict(v=(2 << 40) + 256), dict(kr=1 << 50)):
         assert _write(**kw) == -1, kw
     assert _write(cache=SCALED, k=(6 << 40)) == -1      # over the scales
+    assert _write(cache=dict(v=CACHE["k"])) == -1
+    assert _write(cache={**SCALED, "v_scale": SCALED["k_scale"]}) == -1
 
 
 def test_read_refusals():
@@ -117,6 +119,8 @@ def test_read_refusals():
 def test_commit_refusals():
     for kw in (dict(width=-1), dict(stride=3), dict(paths=None), dict(lens=None)):
         assert _commit(**kw) == -1, kw
+    assert _commit(cache=dict(v=CACHE["k"])) == -1
+    assert _commit(cache={**SCALED, "v_scale": SCALED["k_scale"]}) == -1
 
 
 def test_tree_refusals():
