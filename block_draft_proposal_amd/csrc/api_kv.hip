@@ -229,10 +229,10 @@ int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* b
   if (max_nodes > kMaxNodes) return fail(DFLASH_ERR_UNSUPPORTED, "%s: max_nodes > %d", who, kMaxNodes);
   if (!std::isfinite(scale) || scale <= 0.f || scale > 0x1p100f)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: scale must be > 0 and at most 2^100", who);
+  if (a.c.n_req == 0 || a.c.n_rows == 0) return ok();   // a mask of no rows may be null
   if (mask ? mask_words < (max_nodes + 63) / 64 : mask_words != 0)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: mask_words must be >= ceil(max_nodes / 64) with a mask, 0 without", who);
   if (reinterpret_cast<uintptr_t>(mask) & 7) return fail(DFLASH_ERR_INVALID_ARG, "%s: mask must be 8-byte aligned", who);
-  if (a.c.n_req == 0 || a.c.n_rows == 0) return ok();
   size_t qb = 0;
   if ((st = check_rows(q, q_row_stride, q_head_stride, a.c.n_rows, n_q_heads, a.c.head_dim, 2, qb, "q", who)) != DFLASH_OK)
     return st;

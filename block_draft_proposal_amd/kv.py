@@ -252,6 +252,8 @@ def dflash_tree_attention(q: torch.Tensor, cache: KVCache, *, page_table: torch.
                 not mask.is_contiguous():
             raise ValueError("mask must be contiguous int64 [n_rows, words] on the cache's GPU")
         words = mask.shape[1]
+        if words < (max_nodes + 63) // 64:              # a mask without elements has no address to tell it by
+            raise ValueError("mask must have at least ceil(max_nodes / 64) words")
     if out is None:
         with _on(stream):
             out = torch.empty((n_rows, n_q_heads, head_dim), dtype=torch.bfloat16, device=cache.device)

@@ -139,6 +139,7 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
  *         bf16; pointer and strides multiples of 16 bytes
  *   mask  uint64 [n_rows, mask_words], bit j of word w is node 64 w + j;
  *         mask_words >= ceil(max_nodes / 64); or NULL with mask_words 0
+ *         (neither is looked at in a call without rows or requests)
  *   out   bf16 [n_rows, n_q_heads, head_dim] contiguous, 16-byte aligned; may
  *         not overlap q or the cache
  *   max_nodes  1 .. 4096: no request has more nodes (rows of a request beyond
