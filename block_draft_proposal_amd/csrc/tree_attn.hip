@@ -42,6 +42,7 @@
 // 330, but 16 nodes e4m3 276), two row tiles to a wave (wide 356), sums of the
 // rounded weights (wide 346, error 2.0e-3 for 2.1e-3), steps priced by their
 // rows (256 requests 502 for 484).
+#include <algorithm>
 #include <type_traits>
 
 #include "kv_cache.h"
@@ -979,8 +980,16 @@ auto with_shape(const KvView& c, int rw, const F& f) {
 
 }  // namespace
 
+// The most that any call with up to max_nodes nodes takes, so that a workspace
+// for many nodes serves fewer.  (The forms alone do not grow with their rows:
+// 64 and 128 are 33 KB apart, the smaller the larger.)  A form of rw row waves
+// is for more than 16 rw rows.
 size_t tree_attention_bytes(const KvView& c, int32_t n_req, int32_t max_nodes, int32_t n_q_heads) {
-  return with_shape(c, row_waves(c, max_nodes, n_q_heads / c.n_kv_heads), [](auto l) { return decltype(l)::bytes(); });
+  const int64_t rows = (int64_t)max_nodes * (n_q_heads / c.n_kv_heads);
+  size_t most = 0;
+  for (int rw = 1; rw <= 8 && (rw == 1 || rows > 16 * rw); rw *= 2)
+    most = std::max(most, with_shape(c, rw, [](auto l) { return decltype(l)::bytes(); }));
+  return most;
 }
 
 hipError_t launch_tree_attention(const TreeArgs& a, hipStream_t stream) {

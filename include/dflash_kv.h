@@ -153,7 +153,9 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
  * time; its sums are split by the lengths of the whole batch, so a request
  * may differ in the last bits from one batch to another.
  * Scratch: dflash_tree_attention_workspace_size() bytes, 256-byte aligned; it
- * does not depend on the lengths, so one workspace serves a growing cache.
+ * does not depend on the lengths, so one workspace serves a growing cache, and
+ * never falls with max_nodes, n_req or n_q_heads, so one for the largest values
+ * serves every call on the cache.
  * It may not overlap q, out or the cache, and calls that may run at the same
  * time need one each. */
 size_t dflash_tree_attention_workspace_size(const dflash_kv_cache* cache, int32_t n_req, int32_t max_nodes,

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_draft_proposal_amd as D
-from gpu_helpers import require_gpu, say
+from gpu_helpers import DEV, require_gpu, say
 from test_gpu_tree_attention import build
 
 pytestmark = pytest.mark.gpu
@@ -20,3 +20,19 @@ def test_an_idle_step_with_a_tree_mask():
     with pytest.raises(ValueError, match="words"):
         D.dflash_tree_attention(s["q"], s["cache"], **dict(s["kw"], mask=s["kw"]["mask"][:, :0].contiguous()))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind,dim", [("bf16", 128), ("i8", 64), ("bf16", 256)])
+def test_one_workspace_for_the_largest_tree_serves_every_smaller_one(kind, dim):
+    require_gpu()
+    say(f"kept workspace {kind} {dim}")
+    s = build(kind, [300, 20], [64, 30], 16, 2, 4, dim, "tree", seed=14)
+    size = D.tree_attention_workspace_size(s["cache"], n_req=2, max_nodes=64, n_q_heads=8)
+    work = torch.empty(size, dtype=torch.uint8, device=DEV)
+    off = s["kw"]["offsets"]
+    for nodes in (64, 33, 20, 16, 9, 8, 1):
+        kw = dict(s["kw"], max_nodes=nodes, offsets=torch.stack([off[0], off[0] + nodes, off[0] + nodes + min(nodes, 30)]))
+        out = D.dflash_tree_attention(s["q"], s["cache"], workspace=work, **kw)
+        want = D.dflash_tree_attention(s["q"], s["cache"], **kw)
+        n = nodes + min(nodes, 30)
+        assert torch.equal(out[:n], want[:n]), nodes
