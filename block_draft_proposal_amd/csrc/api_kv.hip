@@ -122,10 +122,30 @@ int check_stream(const KvView& v, const char* who) {
   return DFLASH_OK;
 }
 
-// K and V are written side by side, in no order.
+// Whether two arrays of n pages, `na` bytes each at a + i * sa and `nb` at
+// b + i * sb, share a byte.  Pages of one stride that lie within each other's
+// span are apart where those of b fit the gaps of a; of two strides, they are
+// taken to meet.
+bool pages_meet(const void* a, size_t na, int64_t sa, const void* b, size_t nb, int64_t sb, int64_t n) {
+  if (!overlaps(a, (size_t)(n - 1) * sa + na, b, (size_t)(n - 1) * sb + nb)) return false;
+  if (n == 1 || sa != sb) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const size_t s = (size_t)sa, gap = y >= x ? (y - x) % s : (s - (x - y) % s) % s;   // from a page of a to the next of b
+  return gap < na || gap + nb > s;
+}
+
+// K, V and their scales are written side by side, in no order.
 int check_apart(const KvView& v, const char* who) {
-  if (v.k == v.v || (v.k_scale && v.k_scale == v.v_scale))
-    return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache's K and V are the same memory", who);
+  const size_t rows = (size_t)v.n_kv_heads * v.page_size, codes = rows * v.head_dim * code_bytes(v.dtype);
+  const int64_t n = v.n_pages;
+  if (pages_meet(v.k, codes, v.page_bytes, v.v, codes, v.page_bytes, n) ||
+      (v.k_scale && pages_meet(v.k_scale, rows, v.scale_page_bytes, v.v_scale, rows, v.scale_page_bytes, n)))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache's K and V overlap", who);
+  if (!v.k_scale) return DFLASH_OK;
+  for (const unsigned char* c : {v.k, v.v})
+    for (const uint8_t* s : {v.k_scale, v.v_scale})
+      if (pages_meet(c, codes, v.page_bytes, s, rows, v.scale_page_bytes, n))
+        return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache's scales overlap its K or V", who);
   return DFLASH_OK;
 }
 

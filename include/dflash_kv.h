@@ -90,8 +90,10 @@ typedef struct {
  *         or DFLASH_F32); pointers and strides multiples of 16 bytes; they may
  *         not overlap the cache.
  * n_rows * head_dim is below 2^35 (here and in dflash_kv_read).
- * K and V of the cache may not be the same memory (here and in
- * dflash_kv_commit; the read and the attention take it).
+ * No two of the cache's k, v, k_scale and v_scale may share memory (here and
+ * in dflash_kv_commit; the read and the attention take it).  They may lie in
+ * each other's gaps, as in one pool whose pages hold all four, if they then
+ * have one page stride in bytes.
  * Positions written by one call must be distinct rows of the cache: requests
  * may share pages that they only read, not pages that they write. */
 int dflash_kv_write(const dflash_kv_cache* cache, const dflash_kv_batch* batch, const void* k, int64_t k_row_stride,

@@ -5,6 +5,7 @@ import torch
 
 import block_draft_proposal_amd as D
 from gpu_helpers import DEV, require_gpu, say
+from kv_helpers import TYPES, make_plan, rand_rows
 from test_gpu_tree_attention import build
 
 pytestmark = pytest.mark.gpu
@@ -36,3 +37,60 @@ def test_one_workspace_for_the_largest_tree_serves_every_smaller_one(kind, dim):
         want = D.dflash_tree_attention(s["q"], s["cache"], **kw)
         n = nodes + min(nodes, 30)
         assert torch.equal(out[:n], want[:n]), nodes
+
+
+def _one_pool(kind, n_pages, heads, page, dim, gap):
+    """K, V and their scales side by side in each page of one buffer, `gap`
+    bytes between pages; the buffer, and the cache on it."""
+    codes, scales = heads * page * dim, heads * page
+    whole = -(-(2 * codes + 2 * scales + gap) // 16) * 16
+    pool = torch.full((n_pages * whole,), 77, dtype=torch.uint8, device=DEV)
+    k, v = (pool.view(TYPES[kind]).as_strided((n_pages, heads, page, dim), (whole, page * dim, dim, 1), i * codes) for i in range(2))
+    ks, vs = (pool.as_strided((n_pages, heads, page), (whole, page, 1), 2 * codes + i * scales) for i in range(2))
+    return pool, whole, D.KVCache(k, v, ks, vs)
+
+
+@pytest.mark.parametrize("gap", [0, 32])
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+def test_one_pool_for_codes_and_scales(kind, gap):
+    require_gpu()
+    say(f"one pool {kind} {gap}")
+    heads, page, dim = 3, 20, 64
+    (table, st, off), host, n_pages, n_rows = make_plan([3, 0, 41], [30, 7, 12], page)
+    pool, whole, one = _one_pool(kind, n_pages, heads, page, dim, gap)
+    apart = D.KVCache(*(None if t is None else t.contiguous() for t in (one.k, one.v, one.k_scale, one.v_scale)))
+    k, v = rand_rows(n_rows, heads, dim, "bf16", 41), rand_rows(n_rows, heads, dim, "bf16", 42)
+    paths = torch.tensor([[0, 4, 9, 20], [1, 2, 5, 6], [0, 3, 4, 11]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([4, 3, 4], dtype=torch.int32, device=DEV)
+    for c in (one, apart):
+        D.dflash_kv_write(c, k, v, page_table=table, start=st, offsets=off)
+        D.dflash_kv_commit(c, page_table=table, start=st, paths=paths, path_lens=lens)
+    torch.cuda.synchronize()
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(*(getattr(c, name).contiguous().view(torch.uint8) for c in (one, apart))), name
+    used = 2 * heads * page * (dim + 1)
+    assert (pool.view(n_pages, whole)[:, used:] == 77).all()
+    reads = [D.dflash_kv_read(c, page_table=table, start=st, offsets=off, n_rows=n_rows) for c in (one, apart)]
+    n = int(host[2][-1])
+    for a, b in zip(*reads):
+        assert torch.equal(a[:n], b[:n])
+
+
+def test_overlapping_caches_are_refused_before_anything_is_written():
+    require_gpu()
+    say("overlapping cache")
+    heads, page, dim = 2, 16, 64
+    pool = torch.zeros(8 * heads * page * dim, dtype=torch.bfloat16, device=DEV)
+    need = heads * page * dim
+    make = lambda at: pool.as_strided((3, heads, page, dim), (2 * need, page * dim, dim, 1), at)  # noqa: E731
+    (table, st, off), _, _, n_rows = make_plan([0], [20], page, spare=1)
+    rows = [rand_rows(n_rows, heads, dim, "bf16", i) for i in (1, 2)]
+    paths, lens = torch.tensor([[0, 3]], dtype=torch.int32, device=DEV), torch.tensor([2], dtype=torch.int32, device=DEV)
+    for at in (0, 8, page * dim, need - 8, need + 8):
+        cache = D.KVCache(make(0), make(at))
+        with pytest.raises(D.DFlashError, match="overlap"):
+            D.dflash_kv_write(cache, *rows, page_table=table, start=st, offsets=off)
+        with pytest.raises(D.DFlashError, match="overlap"):
+            D.dflash_kv_commit(cache, page_table=table, start=st, paths=paths, path_lens=lens)
+    torch.cuda.synchronize()
+    assert not pool.any()
