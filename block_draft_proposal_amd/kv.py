@@ -62,6 +62,13 @@ def _fns():
     return _lib
 
 
+def _int32(x: int, name: str) -> int:
+    """ctypes cuts a number to its field's 32 bits without a word."""
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 class KVCache:
     """A cache over tensors the caller owns.  k, v [n_pages, n_kv_heads,
     page_size, head_dim] in bf16, float8_e4m3fn or int8, each page contiguous
@@ -77,6 +84,8 @@ class KVCache:
         n_pages, n_kv_heads, page_size, head_dim = k.shape
         if n_pages < 1:
             raise ValueError("a cache has at least one page")
+        for name, n in (("n_kv_heads", n_kv_heads), ("page_size", page_size), ("head_dim", head_dim)):
+            _int32(n, name)
         scaled = k.dtype != torch.bfloat16
         if scaled != (k_scale is not None) or scaled != (v_scale is not None):
             raise ValueError("k_scale and v_scale belong to the 8-bit caches, and both to those")
@@ -124,7 +133,7 @@ def _i32(t: torch.Tensor, name: str, dim: int, device) -> None:
 def _batch(cache: KVCache, page_table, start, offsets, n_rows: int) -> KVBatchStruct:
     _i32(page_table, "page_table", 2, cache.device)
     _i32(start, "start", 1, cache.device)
-    n_req, width = page_table.shape
+    n_req, width = _int32(page_table.shape[0], "page_table's rows"), _int32(page_table.shape[1], "page_table's width")
     if start.shape[0] != n_req:
         raise ValueError("page_table and start must have one row per request")
     if offsets is not None:
@@ -226,11 +235,12 @@ def dflash_kv_commit(cache: KVCache, *, page_table: torch.Tensor, start: torch.T
         raise ValueError("paths and path_lens must have one row per request")
     stride = paths.stride(0) if paths.shape[0] > 1 else paths.shape[1]
     _call(_fns().dflash_kv_commit, cache, stream, cache.ref, ctypes.byref(batch), paths.data_ptr(), stride,
-          paths.shape[1], path_lens.data_ptr())
+          _int32(paths.shape[1], "paths' width"), path_lens.data_ptr())
 
 
 def tree_attention_workspace_size(cache: KVCache, *, n_req: int, max_nodes: int, n_q_heads: int) -> int:
-    return _fns().dflash_tree_attention_workspace_size(cache.ref, n_req, max_nodes, n_q_heads)
+    return _fns().dflash_tree_attention_workspace_size(cache.ref, _int32(n_req, "n_req"), _int32(max_nodes, "max_nodes"),
+                                                       _int32(n_q_heads, "n_q_heads"))
 
 
 def dflash_tree_attention(q: torch.Tensor, cache: KVCache, *, page_table: torch.Tensor, start: torch.Tensor,
@@ -245,13 +255,15 @@ def dflash_tree_attention(q: torch.Tensor, cache: KVCache, *, page_table: torch.
     are left as they were."""
     _rows(q, "q", cache, None)
     n_rows, n_q_heads, head_dim = q.shape
+    _int32(max_nodes, "max_nodes")
+    _int32(n_q_heads, "n_q_heads")
     batch = _batch(cache, page_table, start, offsets, n_rows)
     words = 0
     if mask is not None:
         if mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] != n_rows or mask.device != cache.device or \
                 not mask.is_contiguous():
             raise ValueError("mask must be contiguous int64 [n_rows, words] on the cache's GPU")
-        words = mask.shape[1]
+        words = _int32(mask.shape[1], "mask's words")
         if words < (max_nodes + 63) // 64:              # a mask without elements has no address to tell it by
             raise ValueError("mask must have at least ceil(max_nodes / 64) words")
     if out is None:
