@@ -78,6 +78,9 @@ bool meets_cache(const KvView& v, const void* p, size_t bytes) {
   return overlaps(p, bytes, v.k_scale, m) || overlaps(p, bytes, v.v_scale, m);
 }
 
+// Whether n rows of int32, `stride` elements apart, lie within the largest extent.
+bool rows_reach(int64_t n, int64_t stride) { return n <= 1 || stride <= kMaxExtent / 8 / n; }
+
 // Checks a batch and fills the view's side of it; rows: the call has dense
 // rows (offsets and n_rows count).
 int view_batch(const dflash_kv_batch* b, bool rows, KvView& v, const char* who) {
@@ -85,6 +88,8 @@ int view_batch(const dflash_kv_batch* b, bool rows, KvView& v, const char* who) 
   if (b->n_req < 0 || b->n_req > (1 << 24)) return fail(DFLASH_ERR_INVALID_ARG, "%s: n_req must be in 0 .. 2^24", who);
   if (b->table_width < 1 || b->table_stride < b->table_width)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: need 1 <= table_width <= table_stride", who);
+  if (!rows_reach(b->n_req, b->table_stride))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the page_table is beyond 2^60 bytes", who);
   if (rows && (b->n_rows < 0 || b->n_rows > INT_MAX))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: n_rows must be in 0 .. 2^31 - 1", who);
   if (b->n_req > 0 && (!b->page_table || !b->start || (rows && b->n_rows > 0 && !b->offsets)))
@@ -213,6 +218,7 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
   if (path_width < 0 || path_stride < path_width)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: need 0 <= path_width <= path_stride", who);
   if (c.n_req == 0 || path_width == 0) return ok();
+  if (!rows_reach(c.n_req, path_stride)) return fail(DFLASH_ERR_INVALID_ARG, "%s: paths is beyond 2^60 bytes", who);
   if ((int64_t)c.n_req * c.n_kv_heads > kMaxThreads / 128)
     return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_req * n_kv_heads must be below 2^25", who);
   if ((st = check_apart(c, who)) != DFLASH_OK) return st;
