@@ -104,6 +104,13 @@ int view_batch(const dflash_kv_batch* b, bool rows, KvView& v, const char* who) 
   return DFLASH_OK;
 }
 
+// Whether [p, p + bytes) meets one of the batch's arrays (n_req > 0).
+bool meets_batch(const KvView& v, const void* p, size_t bytes) {
+  const size_t n = (size_t)v.n_req;
+  return overlaps(p, bytes, v.table, ((n - 1) * (size_t)v.table_stride + v.table_width) * 4) ||
+         overlaps(p, bytes, v.start, n * 4) || overlaps(p, bytes, v.offsets, (n + 1) * 4);
+}
+
 // Strided rows [n_rows, heads, head_dim] of `size`-byte elements: alignment,
 // strides within range, and their extent in bytes.
 int check_rows(const void* p, int64_t row, int64_t head, int64_t n_rows, int32_t heads, int32_t dim, int64_t size,
@@ -204,6 +211,8 @@ int dflash_kv_read(const dflash_kv_cache* cache, const dflash_kv_batch* batch, v
   const size_t n = (size_t)c.n_rows * c.n_kv_heads * c.head_dim * elem_bytes(dtype);
   if (overlaps(k_out, n, v_out, n) || meets_cache(c, k_out, n) || meets_cache(c, v_out, n))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: k_out and v_out overlap each other or the cache", who);
+  if (meets_batch(c, k_out, n) || meets_batch(c, v_out, n))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: k_out or v_out overlaps the batch's arrays", who);
   st = launch_status(launch_kv_read(c, k_out, v_out, dtype, as_hip(stream)), who);
   return st == DFLASH_OK ? ok() : st;
 }
@@ -266,6 +275,9 @@ int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* b
   const size_t ob = (size_t)a.c.n_rows * n_q_heads * a.c.head_dim * 2;
   if (overlaps(out, ob, q, qb) || meets_cache(a.c, out, ob))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: out overlaps q or the cache", who);
+  const size_t mb = mask ? (size_t)a.c.n_rows * mask_words * 8 : 0;
+  if (meets_batch(a.c, out, ob) || overlaps(out, ob, mask, mb))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: out overlaps the batch's arrays or the mask", who);
   const size_t need = tree_attention_bytes(a.c, a.c.n_req, max_nodes, n_q_heads);
   if (workspace_bytes < need || (need && !workspace))
     return fail(DFLASH_ERR_WORKSPACE, "%s: workspace of %zu bytes < %zu needed", who, workspace_bytes, need);
@@ -273,6 +285,8 @@ int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* b
     return fail(DFLASH_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
   if (overlaps(workspace, need, out, ob) || overlaps(workspace, need, q, qb) || meets_cache(a.c, workspace, need))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: the workspace overlaps q, out or the cache", who);
+  if (meets_batch(a.c, workspace, need) || overlaps(workspace, need, mask, mb))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the workspace overlaps the batch's arrays or the mask", who);
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_row_stride;
   a.q_head = q_head_stride;

@@ -106,7 +106,7 @@ int dflash_kv_write(const dflash_kv_cache* cache, const dflash_kv_batch* batch, 
  * a bf16 result of magnitude below 2^-126 is rounded).
  *   k_out, v_out  [n_rows, n_kv_heads, head_dim] contiguous, dtype DFLASH_BF16
  *                 or DFLASH_F32, 16-byte aligned; they may not overlap the
- *                 cache or each other. */
+ *                 cache, each other or the batch's arrays. */
 int dflash_kv_read(const dflash_kv_cache* cache, const dflash_kv_batch* batch, void* k_out, void* v_out,
                    int32_t dtype, dflash_stream_t stream);
 
@@ -143,7 +143,7 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
  *         mask_words >= ceil(max_nodes / 64); or NULL with mask_words 0
  *         (neither is looked at in a call without rows or requests)
  *   out   bf16 [n_rows, n_q_heads, head_dim] contiguous, 16-byte aligned; may
- *         not overlap q or the cache
+ *         not overlap q, mask, the batch's arrays or the cache
  *   max_nodes  1 .. 4096: no request has more nodes (rows of a request beyond
  *         it are left as they were)
  *   scale > 0, at most 2^100
@@ -158,8 +158,8 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
  * does not depend on the lengths, so one workspace serves a growing cache, and
  * never falls with max_nodes, n_req or n_q_heads, so one for the largest values
  * serves every call on the cache.
- * It may not overlap q, out or the cache, and calls that may run at the same
- * time need one each. */
+ * It may not overlap q, out, mask, the batch's arrays or the cache, and calls
+ * that may run at the same time need one each. */
 size_t dflash_tree_attention_workspace_size(const dflash_kv_cache* cache, int32_t n_req, int32_t max_nodes,
                                             int32_t n_q_heads);
 int dflash_tree_attention(const dflash_kv_cache* cache, const dflash_kv_batch* batch, const void* q,
