@@ -11,10 +11,10 @@
 // used.
 //
 // Measured: 64 ragged prompts of up to 2048 rows, 8 heads of 128, bf16 into
-// e4m3 (403 MB read and written) 74.5 us, 5.4 TB/s; 16 contexts of up to 8192
+// e4m3 (403 MB read and written) 74 us, 5.4 TB/s; 16 contexts of up to 8192
 // back in bf16 (407 MB) 73 us, 5.6 TB/s; a copy of 2 GiB runs at 6.0.  The
-// blocks of 32 requests are written in 3.1 us and a path is committed in 3.0,
-// 256 requests' in 6: latency.
+// blocks of 32 requests are written in 3.1 us and a path is committed in 3.2,
+// 256 requests' in 7.0: latency.
 #include "kv_cache.h"
 
 namespace dflash {
@@ -59,8 +59,8 @@ struct RowPlace {
 // A lane's 8 elements of a row of LPR * 8: lane `part` takes 8 consecutive ones
 // of a bf16 dense row, and of an fp32 one 4 in either half, so that each of
 // its two 16-byte accesses is part of one run (int8 to fp32, 16 ragged
-// requests of up to 4096 rows x 8 heads of 128: 74 us, with 8 consecutive 121;
-// fp32 to e4m3, 64 of up to 1024: 70 us, with 8 consecutive 79).
+// requests of up to 4096 rows x 8 heads of 128: 71 to 78 us, with 8 consecutive
+// 142; fp32 to e4m3, 64 of up to 1024: 70 us, with 8 consecutive 78).
 template <int DENSE, int LPR>
 __device__ __forceinline__ int first_of(int part) { return DENSE == DFLASH_F32 ? part * 4 : part * 8; }
 template <int DENSE, int LPR>
@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(KvView c, KvRows in)
   const int units = 2 * c.n_kv_heads, u0 = blockIdx.y * UNITS;
   Eight<SRC, LPR> e[UNITS];
   // Large batches are not in the caches any more when they are read.  Whole
-  // runs of 128 bytes and more pass them by (e4m3 from bf16: 74.5 us, through
-  // them 81; bf16 51 and 55), shorter ones would cost (64 int8: 23.9 and 22.4;
-  // fp32 rows' halves: 74 and 70).
+  // runs of 128 bytes and more pass them by (64 ragged prompts of up to 2048
+  // rows x 8 heads of 128, e4m3 from bf16: 75 us, through them 82; bf16 103 and
+  // 109), shorter ones would cost (64 int8: 23.5 and 22.2), and fp32 rows'
+  // halves do not care (69.5 and 70.5).
   constexpr bool kNt = UNITS > 1 && SRC == DFLASH_BF16 && (DT == DFLASH_BF16 || LPR >= 16);
   const int first = first_of<SRC, LPR>(part), second = second_of<SRC, LPR>(part);
 #pragma unroll
@@ -314,8 +315,8 @@ __global__ void __launch_bounds__(kThreads) kv_commit_kernel(KvView c, const int
 
 // (kv head, K or V) pairs per thread: 4 keep enough loads in flight for the
 // stream (64 ragged prompts into e4m3: 75 us, with 2 93, with 1 137, with 8
-// 75; read back 73, 89, 161, 73); 1 where the batch is too small to fill the
-// chip with 4 (32 blocks of 16: 3.1 us, with 4 3.8).
+// 76; read back 74, 90, 162, 73); 1 where the batch is too small to fill the
+// chip with 4 (32 blocks of 16: 3.5 us, with 4 4.1).
 inline int units_for(int64_t n_rows, int lpr, int n_kv_heads) {
   const int64_t wgs = (n_rows * lpr + kThreads - 1) / kThreads * ((2 * n_kv_heads + 3) / 4);
   return wgs >= 1024 ? 4 : 1;

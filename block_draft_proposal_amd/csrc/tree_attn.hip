@@ -24,24 +24,30 @@
 // equal pieces, one for each workgroup.  A piece that covers an item writes
 // its result; pieces of a cut item leave (m, l, O) in the workspace, at most
 // two to a workgroup, and a second kernel joins them in a fixed order (32
-// requests x 16 nodes, bf16: 71 us and 10).
+// requests x 16 nodes, bf16: 73 us and 10).
 //
 // Loads run two steps ahead of the products and do not stop at an item's end:
 // each step's rows are looked up (page table, then addresses into LDS) by one
 // thread a row, two steps before its direct loads are issued.
 //
-// Measured (pages of 16, 8 kv heads of 128; us, both kernels): 64 requests x
-// 4 nodes x 32 heads over 8160 positions, bf16 383 (5.6 TB/s; a plain read of
-// 2 GiB runs at 6.7), e4m3 209, int8 213 (5.1): bound by HBM.  16 nodes: 396,
-// 263, 300.  8 requests x 64 nodes x 64 heads over 16384: 337, 344, 427 (820,
-// 800, 645 TFLOP/s; a library product of 8192^3 reaches 1430): a wave's chain
-// of products, exponentials and LDS reads, two waves to a SIMD, and for 8-bit
-// types the conversions.  One token over 200 positions: 14, of which a chain of
-// dependent loads (lengths, table, rows) and two launches are most.
-// Tried without gain: a ring of four stages with one barrier a step (wide
-// 330, but 16 nodes e4m3 276), two row tiles to a wave (wide 356), sums of the
-// rounded weights (wide 346, error 2.0e-3 for 2.1e-3), steps priced by their
-// rows (256 requests 502 for 484).
+// Measured (pages of 16, 8 kv heads of 128, all requests alike; us, both
+// kernels, passes in one graph; boxes differ by 2 %): 64 requests x 4 nodes x
+// 32 heads over 8160 positions, bf16 382 (5.6 TB/s; a plain read of 2 GiB runs
+// at 6.7), e4m3 208 (5.2), int8 214 (5.1): bound by HBM, each byte read once.
+// 16 nodes: 396, 262, 302; in int8 the vector units issue for half of the
+// time, mostly conversions.  8 requests x 64 nodes x 64 heads over 16384: 335
+// to 344, 343, 426 (800 to 820, 803, 646 TFLOP/s; a library product of 8192^3
+// reaches 1430): the matrix cores are busy for 31 % of the time, vector units
+// issue for 23, LDS is read for 17: a wave waits in turn for each, two waves to
+// a SIMD.  One token over 200 positions: 14.0, main kernel 27 000 cycles in a
+// row (plan 2400, query and cursor 2700, two iterations that look rows up and
+// issue their loads 3000, their arrival 2700, first step 2100, second step and
+// the join of the key waves 11 100, output 1900, the loop's end 1500).
+// Tried without gain (each beside the kernel of its day, wide: the bf16 shape
+// of 64 nodes above): a ring of four stages with one barrier a step (wide 330
+// for 337, but 16 nodes e4m3 276 for 263), two row tiles to a wave (wide 356
+// for 337), sums of the rounded weights (wide 346 for 337, error 2.0e-3 for
+// 2.1e-3), steps priced by their rows (256 requests 502 for 484).
 #include <algorithm>
 #include <type_traits>
 
@@ -75,8 +81,8 @@ struct Shape {
   static constexpr int kStatsAt = kBadAt + 32;                             // [kKeyWaves][kRows] m, l
   static constexpr int kLds = kStatsAt + 8 * kKeyWaves * kRows;
   // Workgroups of a CU, by their LDS and by registers: two waves to a SIMD,
-  // one with heads of 256 (8 x 64 nodes x 64 heads of 256 over 8192, bf16: 446
-  // us, with pieces for twice as many 480).
+  // one with heads of 256 (8 x 64 nodes x 64 heads of 256 over 8192, bf16: 445
+  // us, with pieces for twice as many 479).
   static constexpr int kPerCu = kLds <= 80 * 1024 && kWaves * (D == 256 ? 2 : 1) <= 4 ? 2 : 1;
   static constexpr int kPartOdd = kRows * (D + 2);                         // a partial: O [kRows][D], m and l of each
   static constexpr int kPartFloats = kPartOdd + 4;                         // row, whether odd values were left out
@@ -101,10 +107,10 @@ struct Shape {
 
 // What an item costs besides its steps, in steps: the first step's latency,
 // the join of the key waves and the output.  (bf16, 32 ragged requests of 16
-// nodes, up to 4096 positions: 85 us, priced at 0 steps 104, at 4 the same.)
+// nodes, up to 4096 positions: 85 us, priced at 0 steps 99, at 4 the same.)
 constexpr int kItemCost = 2;
-// A piece is at least this long.  One token over 2000 positions: 16.4 us, with
-// pieces of 4 19.1, of 1 15.7, but 16 over 4000 22.0, 27.9 and 25.3.
+// A piece is at least this long.  One token over 2000 positions: 16.6 us, with
+// pieces of 4 19.3, of 1 15.7, but 16 over 4000 22.2, 28.3 and 25.6.
 constexpr int kMinPiece = 2;
 // Lengths beyond this, or beyond the page table, have no positions: such a
 // request takes one step, whatever its length claims to be, and is NaN.
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
   // With more than 256 registers the accumulators lie in AGPRs, which only the
   // matrix cores compute with.  Without this, at either end of the rare
   // rescaling, the compiler moves them to VGPRs and back in every step (8 x 64
-  // nodes x 64 heads of 256 over 8192, bf16: 567 us, with it 480).
+  // nodes x 64 heads of 256 over 8192, bf16: 542 us, with it 445).
   auto in_accumulators = [](f32x16_t& x) {
     if constexpr (D == 256) asm volatile("" : "+a"(x));
   };
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
       // The sums keep the maximum they were built with until a row's passes it
       // by 2^8: weights up to 256 are as exact as those up to 1, and most
       // blocks then leave O alone (8 x 64 nodes x 64 heads over 16384, bf16:
-      // 360 us, rescaled at every new maximum 378).
+      // 338 us, rescaled at every new maximum 349).
       if (__any((top - m) * cs > 8.f)) {
         const float next = fmaxf(m, top), keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - next) * cs);
         m = next;
@@ -854,7 +860,7 @@ __global__ void __launch_bounds__((Shape<DT, D, RW>::kThreads), (D == 256 ? 1 : 
 // which piece finished first.  kJoinWgs workgroups for each piece share the
 // rows of its items.  Up to 8 pieces, a thread adds the parts of its 4
 // elements; with more, 16 threads do, and their sums are added in their order.
-// (One workgroup for each: 16 nodes over 4000 positions 55 us, with 4 28.)
+// (One workgroup for each: 16 nodes over 4000 positions 27.7 us, with 4 22.2.)
 constexpr int kJoinWgs = 4;
 
 struct JoinSum {
@@ -928,12 +934,14 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, FastDiv per_
 
 // Row waves, 32 rows each, by the most rows that a request may have for a kv
 // head; the waves left of 4 split the keys.  With 32 rows (e4m3, 16 requests x
-// 8 kv heads over 8192) 1, 2, 4 and 8 row waves take 73, 76, 93 and 132 us,
-// with 64 rows 2, 4 and 8 take 86, 112 and 136, with 128 rows 4 and 8 132 and
-// 142.  8 row waves read K and V once for 256 rows, but leave more of them
+// 8 kv heads over 8192) 1, 2, 4 and 8 row waves take 74, 79, 93 and 133 us,
+// with 64 rows 2, 4 and 8 take 84, 111 and 138, with 128 rows 4 and 8 127 and
+// 143.  8 row waves read K and V once for 256 rows, but leave more of them
 // empty: where the tiles of 128 come in pairs they win (512 rows, 8 x 16384,
-// bf16 360 us against 383), where the last is odd they lose (320 rows, e4m3
-// 335 against 312).  Heads of 256 have no registers for 8.
+// bf16 337 us against 358), where the last is odd they lose (320 rows, e4m3
+// 325 against 299).  Heads of 256 have no registers for 8.  The rows are
+// known to the host as max_nodes alone: a caller that allows many more nodes
+// than it sends pays the difference above.
 int row_waves(const KvView& c, int32_t max_nodes, int32_t group) {
   const int64_t rows = (int64_t)max_nodes * group;
   if (rows <= 64) return rows <= 32 ? 1 : 2;

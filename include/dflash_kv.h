@@ -63,7 +63,8 @@ typedef struct {
 /* A ragged batch: rows offsets[r] .. offsets[r+1]-1 of the call's tensors
  * belong to request r, and row offsets[r] + i is its position start[r] + i.
  * offsets ascend; rows from offsets[n_req] up to n_rows (padding) are neither
- * read nor written. */
+ * read nor written.  A request without rows costs a step of a walk from its
+ * neighbours: long runs of them (tens of thousands) are better left out. */
 typedef struct {
   const int32_t* page_table;  /* row r at page_table + r * table_stride, table_width entries */
   int64_t table_stride;       /* elements, >= table_width */
@@ -145,13 +146,17 @@ int dflash_kv_commit(const dflash_kv_cache* cache, const dflash_kv_batch* batch,
  *   out   bf16 [n_rows, n_q_heads, head_dim] contiguous, 16-byte aligned; may
  *         not overlap q, mask, the batch's arrays or the cache
  *   max_nodes  1 .. 4096: no request has more nodes (rows of a request beyond
- *         it are left as they were)
+ *         it are left as they were).  It also chooses how many of a kv head's
+ *         rows a workgroup takes: give the batch's own largest number, not the
+ *         largest ever.  32 rows in a form for 256 take 1.8 times their time.
  *   scale > 0, at most 2^100
  * n_q_heads is a multiple of n_kv_heads, up to 64 query heads to a kv head.
  * Arithmetic: products exact in fp32, sums, maximum and softmax in fp32; the
  * weights are rounded to bf16 for the product with V, the result once to bf16.
- * The sums keep weights up to 2^8, so |v| * positions has to stay below 2^119:
- * beyond, a result may be an infinity.  A call's result is the same every
+ * The sums keep weights up to 2^8, so |v| * positions, and the scale of any V
+ * row, have to stay below 2^119, and scale * |<q, k>|, and scale times the scale
+ * of any K row, below 2^126: beyond, a result may be an infinity or a NaN.  So
+ * may one that an infinity of the prefix has a part in.  A call's result is the same every
  * time; its sums are split by the lengths of the whole batch, so a request
  * may differ in the last bits from one batch to another.
  * Scratch: dflash_tree_attention_workspace_size() bytes, 256-byte aligned; it
