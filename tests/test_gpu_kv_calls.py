@@ -94,3 +94,36 @@ def test_overlapping_caches_are_refused_before_anything_is_written():
             D.dflash_kv_commit(cache, page_table=table, start=st, paths=paths, path_lens=lens)
     torch.cuda.synchronize()
     assert not pool.any()
+
+
+def test_a_captured_step_that_makes_its_own_tensors():
+    """Write, attention, commit and read in one graph, outputs and workspace
+    made by the calls; every replay on new rows equals eager calls."""
+    require_gpu()
+    say("captured step, own tensors")
+    s, e = (build("e4m3", [300, 20], [9, 5], 16, 2, 4, 128, "tree", seed=22) for _ in range(2))
+    k, v = rand_rows(14, 2, 128, "bf16", 61, packed=False), rand_rows(14, 2, 128, "bf16", 62, packed=False)
+    paths = torch.tensor([[0, 3, 8], [1, 2, 4]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([3, 2], dtype=torch.int32, device=DEV)
+
+    def step(x):
+        batch = {name: x["kw"][name] for name in ("page_table", "start", "offsets")}
+        D.dflash_kv_write(x["cache"], k, v, **batch)
+        out = D.dflash_tree_attention(x["q"], x["cache"], **x["kw"])
+        D.dflash_kv_commit(x["cache"], page_table=batch["page_table"], start=batch["start"], paths=paths, path_lens=lens)
+        return out[:14], *D.dflash_kv_read(x["cache"], n_rows=14, **batch)
+
+    for x in (s, e):
+        step(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(s)
+    for i in range(4):
+        k.copy_(rand_rows(14, 2, 128, "bf16", 70 + i, packed=False))
+        v.copy_(rand_rows(14, 2, 128, "bf16", 80 + i, packed=False))
+        graph.replay()
+        want = step(e)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
