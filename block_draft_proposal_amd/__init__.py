@@ -43,3 +43,12 @@ from .kv import (  # noqa: F401
     dflash_tree_attention,
     tree_attention_workspace_size,
 )
+from .kv_pages import (  # noqa: F401
+    KVPool,
+    KVBounds,
+    dflash_kv_resize,
+    dflash_kv_fork,
+    dflash_kv_compact,
+    dflash_kv_copy_pages,
+    kv_pages_workspace_size,
+)

@@ -1,10 +1,11 @@
 // Host-side checks that the entry points on a paged KV cache share.
 #pragma once
 
+#include <algorithm>
 #include <climits>
 
 #include "api_common.h"
-#include "dflash_kv.h"
+#include "dflash_kv_pages.h"
 #include "kv_cache.h"
 
 namespace dflash {
@@ -147,6 +148,26 @@ inline int check_apart(const KvView& v, const char* who) {
     for (const uint8_t* s : {v.k_scale, v.v_scale})
       if (pages_meet(c, codes, v.page_bytes, s, rows, v.scale_page_bytes, n))
         return fail(DFLASH_ERR_INVALID_ARG, "%s: the cache's scales overlap its K or V", who);
+  return DFLASH_OK;
+}
+
+// Checks the bounds of a pool's pages; their extents in bytes.
+inline int check_bounds(const dflash_page_bounds* b, size_t& code_size, size_t& scale_size, const char* who) {
+  if (!b) return fail(DFLASH_ERR_INVALID_ARG, "%s: null bounds", who);
+  if (b->head_dim != 64 && b->head_dim != 128 && b->head_dim != 256)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: head_dim must be 64, 128 or 256", who);
+  if (b->page_size < 1 || b->page_size > 65536)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: page_size must be in 1 .. 65536", who);
+  if (b->n_kv_heads < 1 || b->n_kv_heads > 1024)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: n_kv_heads must be in 1 .. 1024", who);
+  if (b->n_pages < 1 || b->n_pages > INT_MAX)
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: n_pages must be in 1 .. 2^31 - 1", who);
+  if (!b->codes || !b->scale) return fail(DFLASH_ERR_INVALID_ARG, "%s: null pointer in the bounds", who);
+  if (!aligned16(b->codes)) return fail(DFLASH_ERR_INVALID_ARG, "%s: the bounds' codes must be 16-byte aligned", who);
+  scale_size = (size_t)b->n_pages * b->n_kv_heads;
+  code_size = scale_size * 2 * b->head_dim;
+  if (overlaps(b->codes, code_size, b->scale, scale_size))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: the bounds' codes and scales overlap", who);
   return DFLASH_OK;
 }
 

@@ -1,0 +1,572 @@
+// Page tables, the counts of a pool's pages, and the copies of whole pages.
+//
+// Planning reads the counts once, in chunks of 4096 pages, and the tables'
+// entries that change.  Everything that is shared is an integer sum or a
+// minimum, so that no result depends on an order; which page goes where comes
+// from ranks (the i-th free page, the i-th held page from the top), whose sums
+// over chunks one workgroup makes between two launches.  The steps of a call
+// are launches of their own: a launch is what makes one step's writes visible
+// to all of the next.
+#include <algorithm>
+
+#include "kv_pages.h"
+
+namespace dflash {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 4096;                      // pages of a workgroup: 4 rounds of 4 to a thread
+constexpr int kPlanThreads = 1024;
+
+// --- the workspace ---
+
+struct Plan {                                     // a resize's decision
+  int32_t pages;                                  // free pages that it gives; 0 where nobody grows
+  int32_t grow;                                   // whether requests grow
+};
+struct Grant {                                    // what a request gets
+  int32_t begin;                                  // rank of its first free page
+  int32_t has;                                    // entries that it holds before
+  int32_t copy;                                   // index among the copies, or -1
+};
+struct Claim {                                    // growing requests whose partly filled last page this is
+  int32_t count, first;
+};
+
+constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+inline int64_t chunks_of(int64_t n_pages) { return (n_pages + kChunk - 1) / kChunk; }
+
+struct Space {
+  Plan* plan;
+  int2* per_chunk;                                // (free, held) pages of each chunk, then the sums before it
+  Grant* grants;                                  // resize
+  Claim* claims;                                  // resize: by page
+  int32_t* saved_lens;                            // fork
+  int32_t* saved;                                 // fork: [n_req][table_width]
+  int2* moves;                                    // compact: (held from the top, free from the bottom)
+  size_t bytes;
+  Space(void* base, int64_t n_pages, int32_t n_req, int32_t width) {
+    unsigned char* p = static_cast<unsigned char*>(base);
+    plan = reinterpret_cast<Plan*>(p);
+    per_chunk = reinterpret_cast<int2*>(p + 256);
+    const size_t shared = 256 + up256((size_t)(chunks_of(n_pages) + 1) * sizeof(int2));
+    unsigned char* own = p + shared;
+    grants = reinterpret_cast<Grant*>(own);
+    const size_t grant_bytes = up256((size_t)n_req * sizeof(Grant));
+    claims = reinterpret_cast<Claim*>(own + grant_bytes);
+    const size_t resize = grant_bytes + up256((size_t)n_pages * sizeof(Claim));
+    saved_lens = reinterpret_cast<int32_t*>(own);
+    const size_t lens_bytes = up256((size_t)n_req * 4);
+    saved = reinterpret_cast<int32_t*>(own + lens_bytes);
+    const size_t fork = lens_bytes + up256((size_t)n_req * width * 4);
+    moves = reinterpret_cast<int2*>(own);
+    const size_t compact = up256((size_t)(n_pages / 2 + 1) * sizeof(int2));
+    bytes = shared + (resize > fork ? (resize > compact ? resize : compact) : fork > compact ? fork : compact);
+  }
+};
+
+// --- ranks within a chunk ---
+
+// The counts of 4 neighbouring pages, 1 past the last page: neither free nor,
+// where `held` asks below, held.
+struct Four {
+  int32_t refs[4];
+};
+__device__ __forceinline__ Four load_four(const PagesView& v, int64_t p) {
+  typedef int32_t i32x4_t __attribute__((ext_vector_type(4), aligned(4)));
+  Four f;
+  if (p + 4 <= v.n_pages) {
+    const i32x4_t x = *reinterpret_cast<const i32x4_t*>(v.refs + p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.refs[i] = x[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.refs[i] = p + i < v.n_pages ? v.refs[p + i] : -1;
+  }
+  return f;
+}
+
+// Inclusive sums along a wave.
+__device__ __forceinline__ uint64_t wave_scan_u64(uint64_t x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t y = (uint64_t)__shfl_up((unsigned long long)x, o, 64);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+// Exclusive sums along the workgroup of N threads, and the total.
+template <int N>
+__device__ __forceinline__ uint64_t group_scan(uint64_t x, uint64_t& total) {
+  __shared__ uint64_t sums[N / 64];
+  const int wave = threadIdx.x >> 6;
+  const uint64_t scan = wave_scan_u64(x);
+  __syncthreads();                                // the last call's sums have been read
+  if ((threadIdx.x & 63) == 63) sums[wave] = scan;
+  __syncthreads();
+  uint64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < N / 64; ++i) {
+    if (i < wave) before += sums[i];
+    total += sums[i];
+  }
+  return before + scan - x;
+}
+
+// The thread's pages of the chunk: round k holds base + k * 1024 + 4 * thread
+// and the three behind.  before[k]: pages of the chunk with the property that
+// lie before them.
+template <class F>
+__device__ __forceinline__ void chunk_ranks(const Four (&f)[4], const F& has, int32_t (&before)[4], int32_t& total) {
+  uint64_t x = 0;                                 // 16 bits for each round: at most 4096 in all
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += has(f[k].refs[i]);
+    x |= (uint64_t)n << (16 * k);
+  }
+  uint64_t all;
+  const uint64_t scan = group_scan<kThreads>(x, all);
+  int sum = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    before[k] = sum + (int)((scan >> (16 * k)) & 0xffff);
+    sum += (int)((all >> (16 * k)) & 0xffff);
+  }
+  total = sum;
+}
+__device__ __forceinline__ void load_chunk(const PagesView& v, int64_t base, Four (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = load_four(v, base + k * (4 * kThreads) + 4 * threadIdx.x);
+}
+struct IsFree {
+  __device__ __forceinline__ bool operator()(int32_t r) const { return r == 0; }
+};
+struct IsHeld {
+  __device__ __forceinline__ bool operator()(int32_t r) const { return r > 0; }
+};
+
+// --- resize ---
+
+// What request r does; has < 0: nothing.
+struct Change {
+  int32_t has, needs;
+  bool part;                                      // it grows, and its last page is partly filled
+};
+__device__ __forceinline__ Change change_of(const PagesView& v, const int32_t* want, int r) {
+  const int32_t len = v.lens[r], to = want[r];
+  Change c;
+  c.has = v.entries(len);
+  c.needs = v.entries(to);
+  if (c.needs < 0) c.has = -1;
+  c.part = c.has > 0 && to > len && len != c.has * (int64_t)v.page_size;
+  return c;
+}
+
+// Pages of requests that shrink are let go; the claims of those that grow are
+// cleared.  `parts` workgroups to a request.
+__global__ void __launch_bounds__(kThreads) resize_release_kernel(PagesView v, const int32_t* want, Claim* claims, int parts) {
+  const int r = blockIdx.x / parts, part = blockIdx.x - r * parts;
+  const Change c = change_of(v, want, r);
+  if (c.has < 0) return;
+  int32_t* row = v.table + r * v.table_stride;
+  if (part == 0 && threadIdx.x == 0 && c.part) {
+    const int32_t page = row[c.has - 1];
+    if (v.in_pool(page)) claims[page] = Claim{0, 0x7fffffff};
+  }
+  for (int64_t j = c.needs + (int64_t)part * kThreads + threadIdx.x; j < c.has; j += (int64_t)parts * kThreads) {
+    const int32_t page = row[j];
+    if (v.in_pool(page)) atomicSub(v.refs + page, 1);
+    row[j] = -1;
+  }
+}
+
+// Workgroups below `chunks` count a chunk's free pages (and held ones, for
+// compact); those behind enter the claims of 256 requests each.
+__global__ void __launch_bounds__(kThreads) count_kernel(PagesView v, const int32_t* want, Claim* claims, int2* per_chunk, int chunks) {
+  if ((int)blockIdx.x < chunks) {
+    Four f[4];
+    load_chunk(v, (int64_t)blockIdx.x * kChunk, f);
+    uint64_t x = 0, total;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x += (uint64_t)(f[k].refs[i] == 0) | (uint64_t)(f[k].refs[i] > 0) << 32;
+    group_scan<kThreads>(x, total);
+    if (threadIdx.x == 0) per_chunk[blockIdx.x] = make_int2((int)(uint32_t)total, (int)(total >> 32));
+    return;
+  }
+  const int64_t r = ((int64_t)blockIdx.x - chunks) * kThreads + threadIdx.x;
+  if (r >= v.n_req) return;
+  const Change c = change_of(v, want, (int)r);
+  if (!c.part) return;
+  const int32_t page = v.table[r * v.table_stride + c.has - 1];
+  if (!v.in_pool(page)) return;
+  atomicAdd(&claims[page].count, 1);
+  atomicMin(&claims[page].first, (int)r);
+}
+
+// The sums before each chunk, in place; the totals go to per_chunk[chunks].
+__device__ __forceinline__ int2 scan_chunks(int2* per_chunk, int chunks) {
+  uint64_t run = 0;
+  for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
+    const int c = c0 + (int)threadIdx.x;
+    uint64_t x = 0, total;
+    if (c < chunks) x = (uint32_t)per_chunk[c].x | (uint64_t)(uint32_t)per_chunk[c].y << 32;
+    const uint64_t before = run + group_scan<kPlanThreads>(x, total);
+    if (c < chunks) per_chunk[c] = make_int2((int)(uint32_t)before, (int)(before >> 32));
+    run += total;
+  }
+  if (threadIdx.x == 0) per_chunk[chunks] = make_int2((int)(uint32_t)run, (int)(run >> 32));
+  return make_int2((int)(uint32_t)run, (int)(run >> 32));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesView v, const int32_t* want, Space s, int chunks, int32_t* counts) {
+  const int2 pool = scan_chunks(s.per_chunk, chunks);
+  uint64_t pages = 0, copies = 0;                 // up to 2^20 requests of up to 2^31 entries
+  for (int r0 = 0; r0 < v.n_req; r0 += kPlanThreads) {
+    const int r = r0 + (int)threadIdx.x;
+    Change c{-1, 0, false};
+    uint64_t more = 0;
+    bool copy = false;
+    if (r < v.n_req) {
+      c = change_of(v, want, r);
+      if (c.part) {
+        const int32_t page = v.table[r * v.table_stride + c.has - 1];
+        if (v.in_pool(page)) {
+          const int32_t refs = v.refs[page];
+          const Claim claim = s.claims[page];
+          copy = refs > 1 && !(claim.count == refs && claim.first == r);
+        }
+      }
+      if (c.has >= 0 && c.needs > c.has) more = (uint64_t)(c.needs - c.has);
+    }
+    uint64_t all;
+    // pages in the low 52 bits (1024 requests: below 2^42), copies above
+    const uint64_t before = group_scan<kPlanThreads>((more + copy) | (uint64_t)copy << 52, all);
+    if (r < v.n_req) {
+      const uint64_t begin = pages + (before & ((1ull << 52) - 1));
+      // beyond the pool's size nothing is given, whatever the number
+      s.grants[r] = Grant{(int32_t)min(begin, (uint64_t)0x7fffffff), c.has, copy ? (int32_t)(copies + (before >> 52)) : -1};
+    }
+    pages += all & ((1ull << 52) - 1);
+    copies += all >> 52;
+  }
+  if (threadIdx.x == 0) {
+    const bool enough = pages <= (uint64_t)(uint32_t)pool.x;
+    *s.plan = Plan{enough ? (int32_t)pages : 0, enough};
+    counts[0] = enough ? (int32_t)copies : 0;
+    counts[1] = enough ? 0 : (int32_t)min(pages - (uint64_t)(uint32_t)pool.x, (uint64_t)0x7fffffff);
+  }
+}
+
+// Each free page of a rank below plan.pages goes to the request whose share it
+// lies in.  Workgroups behind the chunks set the lengths.
+__global__ void __launch_bounds__(kThreads) resize_assign_kernel(PagesView v, const int32_t* want, Space s, int chunks, int32_t* copies) {
+  const Plan plan = *s.plan;
+  if ((int)blockIdx.x >= chunks) {
+    const int64_t r = ((int64_t)blockIdx.x - chunks) * kThreads + threadIdx.x;
+    if (r >= v.n_req || s.grants[r].has < 0) return;
+    const int32_t to = want[r];
+    if (plan.grow || to < v.lens[r]) v.lens[r] = to;
+    return;
+  }
+  const int32_t first = s.per_chunk[blockIdx.x].x;
+  if (first >= plan.pages) return;
+  const int64_t base = (int64_t)blockIdx.x * kChunk;
+  Four f[4];
+  load_chunk(v, base, f);
+  int32_t before[4], total;
+  chunk_ranks(f, IsFree(), before, total);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int32_t rank = first + before[k];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (f[k].refs[i] != 0) continue;
+      if (rank >= plan.pages) continue;
+      const int32_t page = (int32_t)(base + k * (4 * kThreads) + 4 * threadIdx.x + i);
+      int lo = 0, hi = v.n_req;                   // the last request that begins at or before this rank
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s.grants[mid].begin <= rank) lo = mid; else hi = mid;
+      }
+      const Grant g = s.grants[lo];
+      int32_t* row = v.table + lo * v.table_stride;
+      int32_t at = rank - g.begin;
+      if (g.copy >= 0) {
+        if (at == 0) {
+          const int32_t old = row[g.has - 1];
+          row[g.has - 1] = page;
+          copies[2 * (int64_t)g.copy] = old;
+          copies[2 * (int64_t)g.copy + 1] = page;
+          atomicSub(v.refs + old, 1);
+        }
+        --at;
+      }
+      if (at >= 0) row[g.has + at] = page;
+      v.refs[page] = 1;
+      ++rank;
+    }
+  }
+}
+
+// --- fork ---
+
+// The row that row r becomes (r: none, it stays; -1: empty).
+__device__ __forceinline__ int fork_source(const PagesView& v, const int32_t* parents, const int32_t* lens, int r) {
+  const int32_t p = parents[r];
+  if (p < 0) return -1;
+  if (p >= v.n_req || v.entries(lens[p]) < 0) return r;
+  return p;
+}
+
+__global__ void __launch_bounds__(kThreads) fork_save_kernel(PagesView v, const int32_t* parents, Space s, int parts) {
+  const int r = blockIdx.x / parts, part = blockIdx.x - r * parts;
+  const int32_t len = v.lens[r];
+  if (part == 0 && threadIdx.x == 0) s.saved_lens[r] = len;
+  if (fork_source(v, parents, v.lens, r) == r) return;   // stays, and is read where it is
+  const int32_t has = v.entries(len);
+  const int32_t* row = v.table + r * v.table_stride;
+  int32_t* to = s.saved + (int64_t)r * v.table_width;
+  for (int64_t j = (int64_t)part * kThreads + threadIdx.x; j < has; j += (int64_t)parts * kThreads) to[j] = row[j];
+}
+
+__global__ void __launch_bounds__(kThreads) fork_apply_kernel(PagesView v, const int32_t* parents, Space s, int parts) {
+  const int r = blockIdx.x / parts, part = blockIdx.x - r * parts;
+  const int from = fork_source(v, parents, s.saved_lens, r);
+  if (from == r) return;
+  const int32_t has = max(v.entries(s.saved_lens[r]), 0);
+  int32_t needs = 0;
+  const int32_t* src = nullptr;
+  if (from >= 0) {
+    needs = v.entries(s.saved_lens[from]);
+    src = fork_source(v, parents, s.saved_lens, from) == from ? v.table + from * v.table_stride
+                                                              : s.saved + (int64_t)from * v.table_width;
+  }
+  int32_t* row = v.table + r * v.table_stride;
+  const int32_t most = max(has, needs);
+  for (int64_t j = (int64_t)part * kThreads + threadIdx.x; j < most; j += (int64_t)parts * kThreads) {
+    const int32_t old = j < has ? row[j] : -1, now = j < needs ? src[j] : -1;
+    if (old != now || j >= has) {
+      if (v.in_pool(old)) atomicSub(v.refs + old, 1);
+      if (v.in_pool(now)) atomicAdd(v.refs + now, 1);
+      row[j] = now;
+    }
+  }
+  if (part == 0 && threadIdx.x == 0) v.lens[r] = from < 0 ? 0 : s.saved_lens[from];
+}
+
+// --- compact ---
+
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Space s, int chunks, int32_t* counts) {
+  const int2 pool = scan_chunks(s.per_chunk, chunks);
+  if (threadIdx.x == 0) {
+    counts[0] = 0;
+    counts[1] = pool.y;
+  }
+}
+
+// moves[i]: the i-th held page from the top and the i-th free one from the bottom.
+__global__ void __launch_bounds__(kThreads) compact_list_kernel(PagesView v, Space s, int chunks, int32_t max_moves, int32_t* page_map) {
+  const int2 first = s.per_chunk[blockIdx.x], pool = s.per_chunk[chunks];
+  const int32_t most = min(max_moves, min(pool.x, pool.y));
+  const int64_t base = (int64_t)blockIdx.x * kChunk;
+  Four f[4];
+  load_chunk(v, base, f);
+  int32_t free_before[4], held_before[4], total;
+  chunk_ranks(f, IsFree(), free_before, total);
+  chunk_ranks(f, IsHeld(), held_before, total);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int32_t up = first.x + free_before[k], down = pool.y - 1 - (first.y + held_before[k]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t page = base + k * (4 * kThreads) + 4 * threadIdx.x + i;
+      if (page >= v.n_pages) continue;
+      const int32_t refs = f[k].refs[i];
+      page_map[page] = refs == 0 ? -1 : (int32_t)page;
+      if (refs == 0) {
+        if (up < most) s.moves[up].y = (int32_t)page;
+        ++up;
+      } else if (refs > 0) {
+        if (down < most) s.moves[down].x = (int32_t)page;
+        --down;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) compact_move_kernel(PagesView v, Space s, int chunks, int32_t max_moves, int32_t* page_map,
+                                                                int32_t* copies, int32_t* counts) {
+  const int2 pool = s.per_chunk[chunks];
+  const int32_t most = min(max_moves, min(pool.x, pool.y));
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= most) return;
+  const int2 m = s.moves[i];
+  if (m.x <= m.y) return;                         // sources fall and targets rise: from here on none moves
+  copies[2 * i] = m.x;
+  copies[2 * i + 1] = m.y;
+  page_map[m.x] = m.y;
+  v.refs[m.y] = v.refs[m.x];
+  v.refs[m.x] = 0;
+  bool last = i + 1 >= most;
+  if (!last) {
+    const int2 next = s.moves[i + 1];
+    last = next.x <= next.y;
+  }
+  if (last) counts[0] = (int32_t)(i + 1);
+}
+
+__global__ void __launch_bounds__(kThreads) compact_tables_kernel(PagesView v, const int32_t* page_map, int parts) {
+  const int r = blockIdx.x / parts, part = blockIdx.x - r * parts;
+  const int32_t has = v.entries(v.lens[r]);
+  int32_t* row = v.table + r * v.table_stride;
+  for (int64_t j = (int64_t)part * kThreads + threadIdx.x; j < has; j += (int64_t)parts * kThreads) {
+    const int32_t page = row[j];
+    if (!v.in_pool(page)) continue;
+    const int32_t to = page_map[page];
+    if (to >= 0 && to != page) row[j] = to;
+  }
+}
+
+// --- copies of whole pages ---
+
+// K and V go in pieces of kPiece bytes, 4 x 16 bytes to a thread, all loaded
+// before the first is stored; a pair's last unit is the small arrays.
+constexpr int kPiece = 4 * 16 * kThreads;
+
+struct PageArrays {
+  unsigned char* base[4];                         // k_scale, v_scale, bounds' codes and scales; null: none
+  int64_t stride[4], bytes[4];
+};
+
+__device__ __forceinline__ void copy_bytes(unsigned char* to, const unsigned char* from, int64_t n) {
+  if ((((uintptr_t)to | (uintptr_t)from | (uintptr_t)n) & 15) == 0) {
+    for (int64_t i = threadIdx.x * 16; i < n; i += 16 * kThreads) st16(to + i, ld16(from + i));
+  } else {
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) to[i] = from[i];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) copy_pages_kernel(KvView c, PageArrays small, const int32_t* copies, int64_t max_copies,
+                                                              const int32_t* counts, int64_t row_bytes, int32_t pieces) {
+  const int64_t n = counts ? min((int64_t)max(counts[0], 0), max_copies) : max_copies;
+  const int32_t units = 2 * pieces + 1;           // of a pair
+  for (int64_t u = blockIdx.x; u < n * units; u += gridDim.x) {
+    const int64_t pair = u / units;
+    const int32_t unit = (int32_t)(u - pair * units);
+    const int64_t from = copies[2 * pair], to = copies[2 * pair + 1];
+    if (from < 0 || from >= c.n_pages || to < 0 || to >= c.n_pages || from == to) continue;
+    if (unit < 2 * pieces) {
+      unsigned char* base = unit < pieces ? c.k : c.v;
+      const int64_t at = (int64_t)(unit < pieces ? unit : unit - pieces) * kPiece + threadIdx.x * 16;
+      const unsigned char* src = base + from * c.page_bytes + at;
+      unsigned char* dst = base + to * c.page_bytes + at;
+      u32x4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at + i * 16 * kThreads < row_bytes) w[i] = ld16_nt(src + i * 16 * kThreads);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at + i * 16 * kThreads < row_bytes) st16_nt(dst + i * 16 * kThreads, w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (small.base[i]) copy_bytes(small.base[i] + to * small.stride[i], small.base[i] + from * small.stride[i], small.bytes[i]);
+    }
+  }
+}
+
+// Workgroups to a request: enough of them for the chip where there are few
+// requests, and no more than a row's entries can use.
+int parts_of(const PagesView& v) {
+  const int by_width = (int)(((int64_t)v.table_width + kThreads - 1) / kThreads), by_req = std::max(1, 1024 / std::max(1, v.n_req));
+  return std::min(by_width, by_req);
+}
+unsigned request_groups(const PagesView& v) { return (unsigned)((v.n_req + kThreads - 1) / kThreads); }
+
+}  // namespace
+
+size_t kv_pages_workspace(int64_t n_pages, int32_t n_req, int32_t table_width) {
+  return Space(nullptr, n_pages, n_req, table_width).bytes;
+}
+
+hipError_t launch_kv_resize(const PagesView& v, const int32_t* want, int32_t* copies, int32_t* counts, void* workspace,
+                            hipStream_t stream) {
+  const Space s(workspace, v.n_pages, v.n_req, v.table_width);
+  const int chunks = (int)chunks_of(v.n_pages), parts = parts_of(v);
+  const unsigned groups = request_groups(v);
+  hipError_t e;
+  if (v.n_req > 0) {                              // without requests the call still sets counts
+    resize_release_kernel<<<(unsigned)v.n_req * parts, kThreads, 0, stream>>>(v, want, s.claims, parts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  count_kernel<<<chunks + groups, kThreads, 0, stream>>>(v, want, s.claims, s.per_chunk, chunks);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  resize_plan_kernel<<<1, kPlanThreads, 0, stream>>>(v, want, s, chunks, counts);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  resize_assign_kernel<<<chunks + groups, kThreads, 0, stream>>>(v, want, s, chunks, copies);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const PagesView& v, const int32_t* parents, void* workspace, hipStream_t stream) {
+  const Space s(workspace, v.n_pages, v.n_req, v.table_width);
+  const int parts = parts_of(v);
+  fork_save_kernel<<<(unsigned)v.n_req * parts, kThreads, 0, stream>>>(v, parents, s, parts);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  fork_apply_kernel<<<(unsigned)v.n_req * parts, kThreads, 0, stream>>>(v, parents, s, parts);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_compact(const PagesView& v, int32_t* page_map, int32_t* copies, int64_t max_copies,
+                             int32_t* counts, void* workspace, hipStream_t stream) {
+  const Space s(workspace, v.n_pages, v.n_req, v.table_width);
+  const int chunks = (int)chunks_of(v.n_pages);
+  const int32_t max_moves = (int32_t)std::min<int64_t>(max_copies, v.n_pages / 2);
+  count_kernel<<<chunks, kThreads, 0, stream>>>(v, nullptr, nullptr, s.per_chunk, chunks);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(s, chunks, counts);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  compact_list_kernel<<<chunks, kThreads, 0, stream>>>(v, s, chunks, max_moves, page_map);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (max_moves > 0) {
+    compact_move_kernel<<<(unsigned)((max_moves + kThreads - 1) / kThreads), kThreads, 0, stream>>>(v, s, chunks, max_moves, page_map, copies, counts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (v.n_req > 0) {
+    const int parts = parts_of(v);
+    compact_tables_kernel<<<(unsigned)v.n_req * parts, kThreads, 0, stream>>>(v, page_map, parts);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+hipError_t launch_kv_copy_pages(const KvView& c, const dflash_page_bounds* bounds, const int32_t* copies,
+                                int64_t max_copies, const int32_t* counts, hipStream_t stream) {
+  const int64_t rows = (int64_t)c.n_kv_heads * c.page_size, row_bytes = rows * c.head_dim * (c.dtype == DFLASH_BF16 ? 2 : 1);
+  PageArrays small{};
+  if (c.k_scale) {
+    small.base[0] = c.k_scale;
+    small.base[1] = c.v_scale;
+    small.stride[0] = small.stride[1] = c.scale_page_bytes;
+    small.bytes[0] = small.bytes[1] = rows;
+  }
+  if (bounds) {
+    small.base[2] = reinterpret_cast<unsigned char*>(bounds->codes);
+    small.base[3] = bounds->scale;
+    small.stride[2] = small.bytes[2] = (int64_t)c.n_kv_heads * 2 * c.head_dim;
+    small.stride[3] = small.bytes[3] = c.n_kv_heads;
+  }
+  const int32_t pieces = (int32_t)((row_bytes + kPiece - 1) / kPiece);
+  const int64_t units = max_copies * (2 * (int64_t)pieces + 1);
+  copy_pages_kernel<<<(unsigned)std::min<int64_t>(units, 4096), kThreads, 0, stream>>>(c, small, copies, max_copies, counts, row_bytes, pieces);
+  return hipGetLastError();
+}
+
+}  // namespace dflash
