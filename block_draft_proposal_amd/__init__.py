@@ -52,3 +52,10 @@ from .kv_pages import (  # noqa: F401
     dflash_kv_copy_pages,
     kv_pages_workspace_size,
 )
+from .kv_sparse import (  # noqa: F401
+    dflash_kv_bounds,
+    dflash_kv_select,
+    dflash_sparse_attention,
+    kv_select_workspace_size,
+    sparse_attention_workspace_size,
+)

@@ -22,35 +22,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The request that row t of a ragged batch belongs to and the row's position;
-// false for padding.  t0 is the first row of the wave (uniform): a 64-ary
-// search of offsets finds its request, two steps for up to 4096 requests, and
-// later rows of the wave walk on from there.
-__device__ __forceinline__ bool kv_row_position(const KvView& c, int64_t t0, int64_t t, int32_t& req, int64_t& pos) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, n = c.n_req;                       // the largest r in [lo, lo + n) with offsets[r] <= t0
-  while (n > 1) {
-    const int step = (n + 63) >> 6;
-    const int r = lo + lane * step;
-    const bool at_or_before = lane * step < n && c.offsets[r] <= t0;
-    const uint64_t b = __ballot(at_or_before);
-    const int i = b ? 63 - __builtin_clzll(b) : 0;
-    n = min(step, n - i * step);
-    lo += i * step;
-  }
-  req = lo;
-  if (t >= c.n_rows) return false;
-  int64_t first = c.offsets[req], end = c.offsets[req + 1];
-  while (t >= end && req + 1 < c.n_req) {
-    ++req;
-    first = end;
-    end = c.offsets[req + 1];
-  }
-  if (t < first || t >= end) return false;
-  pos = (int64_t)c.start[req] + (t - first);
-  return true;
-}
-
 struct RowPlace {
   int64_t page;
   int32_t slot;

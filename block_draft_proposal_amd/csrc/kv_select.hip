@@ -1,0 +1,322 @@
+// The pages that a query row may need most, by the bounds of their keys.
+//
+// Two launches.  The first is a small matrix product in integers: for a tile of
+// up to 16 rows of the batch and one kv head, Q' [heads x rows, 2 D] times the
+// bounds [2 D, blocks] by v_mfma_i32_16x16x64_i8, Q' holding the negative part
+// of a row's codes against the least keys and the positive part against the
+// greatest.  The largest of the group's heads becomes an order-preserving key in
+// the workspace.  The second takes each (row, kv head)'s n_take largest keys:
+// the threshold digit by digit from a histogram in LDS, then the blocks in order.
+#include <algorithm>
+
+#include "kv_sparse.h"
+
+namespace dflash {
+namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr uint32_t kForced = 0xffffffffu, kBroken = 0xfffffffeu;
+constexpr int kWaveBlocks = 64;                   // blocks of a wave's step: 4 tiles of 16
+constexpr int kStepBlocks = kWaveBlocks * kThreads / 64;
+
+// NT rows of the batch and 16 / NT heads make the 16 rows of a product; row
+// h * NT + node of step s is head s * (16 / NT) + h of that node.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, FastDiv per_group, int steps, int chunk_blocks, int chunks) {
+  constexpr int kHeads = 16 / NT, kOps = 2 * D / 64;
+  extern __shared__ __align__(16) int8_t queries[];   // [steps][kOps][64 lanes] x 16 bytes: the operands as they lie
+  const KvView& c = a.c;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = per_group.d;
+  // consecutive workgroups take the kv heads of the same blocks
+  const int head = blockIdx.x % c.n_kv_heads;
+  const int rest = blockIdx.x / c.n_kv_heads, chunk = rest % chunks;
+  const int64_t row0 = (int64_t)(rest / chunks) * NT;
+
+  // queries in 8 bits: a wave takes a row at a time
+  for (int n = wave; n < NT; n += kThreads / 64) {
+    const int64_t row = min(row0 + n, c.n_rows - 1);
+    const uint16_t* qp = a.q + row * a.q_row + (int64_t)head * group * a.q_head;
+    constexpr int kVecs = D / 8;                  // 16-byte pieces of a head
+    uint32_t top = 0;
+    for (int x = lane; x < group * kVecs; x += 64) {
+      float f[8];
+      unpack16(ld16(qp + (int64_t)(x / kVecs) * a.q_head + (x % kVecs) * 8), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    }
+    top = wave_max_u32(top);
+    const bool finite = top < 0x7f800000u;
+    const int byte = finite ? max((int)((top + 0x1ffffu) >> 23) - 6, 27) : 127;
+    const float inv = finite ? __uint_as_float((uint32_t)(254 - byte) << 23) : 0.f;
+    for (int x = lane; x < steps * kHeads * kVecs; x += 64) {
+      const int h = min(x / kVecs, group - 1), d = (x % kVecs) * 8;   // heads past the group repeat its last
+      float f[8];
+      unpack16(ld16(qp + (int64_t)h * a.q_head + d), f);
+      uint32_t neg[2] = {0, 0}, pos[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // adding 1.5 * 2^23 rounds to an integer, ties to even, whose two's
+        // complement is then in the sum's low bits
+        const int code = finite ? (int)(__float_as_uint(f[j] * inv + 12582912.f) << 16) >> 16 : 0;
+        neg[j >> 2] |= ((uint32_t)min(code, 0) & 255u) << (8 * (j & 3));
+        pos[j >> 2] |= ((uint32_t)max(code, 0) & 255u) << (8 * (j & 3));
+      }
+      const int slot = x / kVecs, step = slot / kHeads, m = (slot % kHeads) * NT + n;
+      // byte k of the contraction: operand k / 64, lane group k % 64 / 16
+      int8_t* at = queries + ((step * kOps + d / 64) * 64 + (d % 64 / 16) * 16 + m) * 16 + d % 16;
+      *reinterpret_cast<uint2*>(at) = make_uint2(neg[0], neg[1]);
+      *reinterpret_cast<uint2*>(at + (D / 64) * 64 * 16) = make_uint2(pos[0], pos[1]);
+    }
+  }
+  __syncthreads();
+
+  // the requests whose rows the tile holds
+  int32_t req = 0;
+  int64_t pos = 0, row = row0;
+  kv_row_position(c, row0, row0, req, pos);
+  for (; row < min(row0 + NT, c.n_rows) && req < c.n_req; ++req) {
+    const int64_t first = c.offsets[req], end = min((int64_t)c.offsets[req + 1], min(first + a.max_nodes, c.n_rows));
+    const int64_t next = max(row, (int64_t)c.offsets[req + 1]);
+    if (max(first, row) >= end) {
+      row = next;
+      continue;
+    }
+    const int lo = (int)(max(first, row) - row0), hi = (int)(min(end, row0 + NT) - row0);   // its rows of the tile
+    row = next;
+    const int32_t blocks = kv_blocks(c, c.start[req]);
+    const int32_t* table = c.table + req * c.table_stride;
+    const int32_t to = (int32_t)min((int64_t)blocks, ((int64_t)chunk + 1) * chunk_blocks);
+    for (int64_t b0 = (int64_t)chunk * chunk_blocks + wave * kWaveBlocks; b0 < to; b0 += kStepBlocks) {
+      i32x4_t edge[4][kOps];
+      uint32_t byte[4];
+      bool broken[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int32_t b = (int32_t)min(b0 + 16 * t + (lane & 15), (int64_t)blocks - 1);
+        int32_t id = table[b];
+        broken[t] = id < 0 || id >= c.n_pages;
+        if (broken[t]) id = 0;
+        const int64_t at = (int64_t)id * c.n_kv_heads + head;
+        const int8_t* p = a.codes + at * (2 * D) + (lane >> 4) * 16;
+#pragma unroll
+        for (int o = 0; o < kOps; ++o) edge[t][o] = *reinterpret_cast<const i32x4_t*>(p + 64 * o);
+        byte[t] = a.scale[at];
+      }
+      int best[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) best[t][i] = -0x7fffffff - 1;
+      for (int s = 0; s < steps; ++s) {
+        i32x4_t q[kOps];
+#pragma unroll
+        for (int o = 0; o < kOps; ++o) q[o] = *reinterpret_cast<const i32x4_t*>(queries + ((s * kOps + o) * 64 + lane) * 16);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          i32x4_t sum = {0, 0, 0, 0};
+#pragma unroll
+          for (int o = 0; o < kOps; ++o) sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(q[o], edge[t][o], sum, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) best[t][i] = max(best[t][i], sum[i]);
+        }
+      }
+      // sum[i] of lane l is row 4 (l / 16) + i of the product and block l % 16
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (NT <= 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) best[t][i] = max(best[t][i], __shfl_xor(best[t][i], 32, 64));
+        }
+        if constexpr (NT <= 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) best[t][i] = max(best[t][i], __shfl_xor(best[t][i], 16, 64));
+        }
+        if constexpr (NT <= 2) {
+          best[t][0] = max(best[t][0], best[t][2]);
+          best[t][1] = max(best[t][1], best[t][3]);
+        }
+        if constexpr (NT == 1) best[t][0] = max(best[t][0], best[t][1]);
+        const int64_t b = b0 + 16 * t + (lane & 15);
+        // whole numbers below 2^23 times a power of two: exact, and normal
+        // numbers for any scale byte from 27 on once 2^-20 is taken off
+        const float unit = kv_scale_value(byte[t] == 255u ? 127u : (uint32_t)max((int)byte[t] - 20, 0));
+        constexpr int kRegs = NT < 4 ? NT : 4;
+        const int groups = NT < 4 ? 1 : NT / 4;   // lane groups that hold rows of their own
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) {
+          const int n = 4 * (lane >> 4) + i;
+          if ((lane >> 4) >= groups || n < lo || n >= hi || b >= to) continue;
+          const uint32_t bits = __float_as_uint((float)best[t][i] * unit);
+          uint32_t key = (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
+          if (broken[t] || byte[t] == 255u) key = kBroken;
+          if (b < a.n_first || b >= blocks - a.n_last) key = kForced;
+          a.keys[((row0 + n) * c.n_kv_heads + head) * c.table_width + b] = key;
+        }
+      }
+    }
+  }
+}
+
+// --- the choice ---
+
+constexpr int kDigits = 2048;                     // bins: digits of 11, 11 and 10 bits from the top
+constexpr int kOwn = 16;                          // keys of a thread in a segment, neighbours
+constexpr int kSegment = kOwn * kThreads;
+
+__device__ __forceinline__ uint32_t digit(uint32_t key, int pass) {
+  return pass == 0 ? key >> 21 : pass == 1 ? (key >> 10) & 2047u : key & 1023u;
+}
+__device__ __forceinline__ uint32_t prefix_mask(int pass) { return pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u; }
+
+// The thread's keys of the segment at s0; `n` of them are there.
+__device__ __forceinline__ int load_keys(const uint32_t* keys, int64_t s0, int32_t blocks, uint32_t (&k)[kOwn]) {
+  const int64_t at = s0 + (int64_t)threadIdx.x * kOwn;
+  const int n = (int)max((int64_t)0, min((int64_t)kOwn, blocks - at));
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) k[i] = i < n ? keys[at + i] : 0u;
+  return n;
+}
+
+// Exclusive sums of two 16-bit counts along the workgroup, and the totals.
+__device__ __forceinline__ uint32_t scan_counts(uint32_t x, uint32_t& total, uint32_t* sums) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t scan = x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t y = (uint32_t)__shfl_up((int)scan, o, 64);
+    if (lane >= o) scan += y;
+  }
+  __syncthreads();
+  if (lane == 63) sums[wave] = scan;
+  __syncthreads();
+  uint32_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) {
+    if (i < wave) before += sums[i];
+    total += sums[i];
+  }
+  return before + scan - x;
+}
+
+__global__ void __launch_bounds__(kThreads) select_take_kernel(SelectArgs a) {
+  __shared__ uint32_t bins[kDigits];
+  __shared__ uint32_t sums[kThreads / 64];
+  __shared__ uint32_t found[2];
+  const KvView& c = a.c;
+  const int64_t row = blockIdx.x / c.n_kv_heads;
+  const int head = blockIdx.x - (unsigned)row * c.n_kv_heads;
+  int32_t req = 0;
+  int64_t pos = 0;
+  if (!kv_row_position(c, row, row, req, pos) || row - c.offsets[req] >= a.max_nodes) return;   // the same in every thread
+  const int32_t blocks = kv_blocks(c, c.start[req]), take = a.n_take;
+  int32_t* out = a.out + ((int64_t)row * c.n_kv_heads + head) * take;
+  if (blocks <= take) {
+    for (int i = threadIdx.x; i < take; i += kThreads) out[i] = i < blocks ? i : -1;
+    return;
+  }
+  const uint32_t* keys = a.keys + ((int64_t)row * c.n_kv_heads + head) * c.table_width;
+  uint32_t k[kOwn];
+  int n = load_keys(keys, 0, blocks, k);
+  // the threshold: the take-th largest key, a digit at a time from the top
+  uint32_t threshold = 0, left = (uint32_t)take;  // keys still to be taken among those that agree so far
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) bins[i] = 0;
+    __syncthreads();
+    for (int64_t s0 = 0; s0 < blocks; s0 += kSegment) {
+      if (blocks > kSegment) n = load_keys(keys, s0, blocks, k);
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i)
+        if (i < n && ((k[i] ^ threshold) & prefix_mask(pass)) == 0) atomicAdd(&bins[digit(k[i], pass)], 1u);
+    }
+    __syncthreads();
+    // thread t holds bins 2047 - 8 t down to 2040 - 8 t
+    uint32_t own[8], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      own[i] = bins[kDigits - 1 - (int)threadIdx.x * 8 - i];
+      sum += own[i];
+    }
+    uint32_t above = scan_counts(sum, total, sums);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (above < left && above + own[i] >= left) {
+        found[0] = kDigits - 1 - threadIdx.x * 8 - i;
+        found[1] = left - above;
+      }
+      above += own[i];
+    }
+    __syncthreads();
+    threshold |= found[0] << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
+    left = found[1];
+  }
+  // blocks above the threshold, and the first `left` at it, in order
+  uint32_t base_above = 0, base_at = 0;
+  for (int64_t s0 = 0; s0 < blocks; s0 += kSegment) {
+    if (blocks > kSegment) n = load_keys(keys, s0, blocks, k);
+    uint32_t x = 0, total;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (i < n) x += k[i] > threshold ? 1u : k[i] == threshold ? 0x10000u : 0u;
+    const uint32_t before = scan_counts(x, total, sums);
+    uint32_t above = base_above + (before & 0xffffu), at = base_at + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      if (i >= n) continue;
+      const bool is_above = k[i] > threshold, is_at = k[i] == threshold;
+      if (is_above || (is_at && at < left)) out[above + min(at, left)] = (int32_t)(s0 + threadIdx.x * kOwn + i);
+      above += is_above;
+      at += is_at;
+    }
+    base_above += total & 0xffffu;
+    base_at += total >> 16;
+  }
+}
+
+template <int D, int NT>
+hipError_t score(const SelectArgs& a, hipStream_t s) {
+  const FastDiv per_group = FastDiv::make(a.n_q_heads / a.c.n_kv_heads);
+  const int steps = (per_group.d + 16 / NT - 1) / (16 / NT);
+  const int64_t tiles = (a.c.n_rows + NT - 1) / NT * a.c.n_kv_heads;
+  // blocks of a workgroup: as many as leave 1024 workgroups, so that the
+  // queries are prepared seldom
+  int64_t chunk = kStepBlocks;
+  while (chunk < a.c.table_width && tiles * ((a.c.table_width + 2 * chunk - 1) / (2 * chunk)) >= 1024) chunk *= 2;
+  const int chunks = (int)((a.c.table_width + chunk - 1) / chunk);
+  const size_t lds = (size_t)steps * (2 * D / 64) * 1024;
+  select_score_kernel<D, NT><<<(unsigned)(tiles * chunks), kThreads, lds, s>>>(a, per_group, steps, (int)chunk, chunks);
+  return hipGetLastError();
+}
+template <int D>
+hipError_t score_dim(const SelectArgs& a, hipStream_t s) {
+  // rows of a tile: as few as hold a request, for the rest of the product is
+  // filled with heads; and no more than 64 KB of operands hold
+  const int group = a.n_q_heads / a.c.n_kv_heads;
+  int rows = 16;
+  while (rows > 1 && (rows / 2 >= a.max_nodes || (int64_t)group * rows * D > 32768)) rows /= 2;
+  if (rows == 1) return score<D, 1>(a, s);
+  if (rows == 2) return score<D, 2>(a, s);
+  if (rows == 4) return score<D, 4>(a, s);
+  if (rows == 8) return score<D, 8>(a, s);
+  return score<D, 16>(a, s);
+}
+
+}  // namespace
+
+size_t kv_select_bytes(int64_t n_rows, int32_t n_kv_heads, int32_t table_width) {
+  return ((size_t)n_rows * n_kv_heads * table_width * 4 + 255) / 256 * 256;
+}
+
+hipError_t launch_kv_select(const SelectArgs& a, hipStream_t stream) {
+  const hipError_t e = a.c.head_dim == 64    ? score_dim<64>(a, stream)
+                       : a.c.head_dim == 128 ? score_dim<128>(a, stream)
+                                             : score_dim<256>(a, stream);
+  if (e != hipSuccess) return e;
+  select_take_kernel<<<(unsigned)(a.c.n_rows * a.c.n_kv_heads), kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace dflash
