@@ -1,6 +1,6 @@
 // Page tables, the counts of a pool's pages, and the copies of whole pages.
 //
-// Planning reads the counts once, in chunks of 4096 pages, and the tables'
+// Planning reads the counts once, in chunks of 1024 pages, and the tables'
 // entries that change.  Everything that is shared is an integer sum or a
 // minimum, so that no result depends on an order; which page goes where comes
 // from ranks (the i-th free page, the i-th held page from the top), whose sums
@@ -15,7 +15,7 @@ namespace dflash {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 4096;                      // pages of a workgroup: 4 rounds of 4 to a thread
+constexpr int kChunk = 4 * kThreads;              // pages of a workgroup: 4 neighbours to a thread
 constexpr int kPlanThreads = 1024;
 
 // --- the workspace ---
@@ -115,32 +115,15 @@ __device__ __forceinline__ uint64_t group_scan(uint64_t x, uint64_t& total) {
   return before + scan - x;
 }
 
-// The thread's pages of the chunk: round k holds base + k * 1024 + 4 * thread
-// and the three behind.  before[k]: pages of the chunk with the property that
-// lie before them.
+// The chunk's pages with the property before the thread's four, and in all.
 template <class F>
-__device__ __forceinline__ void chunk_ranks(const Four (&f)[4], const F& has, int32_t (&before)[4], int32_t& total) {
-  uint64_t x = 0;                                 // 16 bits for each round: at most 4096 in all
+__device__ __forceinline__ int32_t chunk_ranks(const Four& f, const F& has, int32_t& total) {
+  uint64_t n = 0, all;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n += has(f[k].refs[i]);
-    x |= (uint64_t)n << (16 * k);
-  }
-  uint64_t all;
-  const uint64_t scan = group_scan<kThreads>(x, all);
-  int sum = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    before[k] = sum + (int)((scan >> (16 * k)) & 0xffff);
-    sum += (int)((all >> (16 * k)) & 0xffff);
-  }
-  total = sum;
-}
-__device__ __forceinline__ void load_chunk(const PagesView& v, int64_t base, Four (&f)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) f[k] = load_four(v, base + k * (4 * kThreads) + 4 * threadIdx.x);
+  for (int i = 0; i < 4; ++i) n += has(f.refs[i]);
+  const int32_t before = (int32_t)group_scan<kThreads>(n, all);
+  total = (int32_t)all;
+  return before;
 }
 struct IsFree {
   __device__ __forceinline__ bool operator()(int32_t r) const { return r == 0; }
@@ -188,13 +171,10 @@ __global__ void __launch_bounds__(kThreads) resize_release_kernel(PagesView v, c
 // compact); those behind enter the claims of 256 requests each.
 __global__ void __launch_bounds__(kThreads) count_kernel(PagesView v, const int32_t* want, Claim* claims, int2* per_chunk, int chunks) {
   if ((int)blockIdx.x < chunks) {
-    Four f[4];
-    load_chunk(v, (int64_t)blockIdx.x * kChunk, f);
+    const Four f = load_four(v, (int64_t)blockIdx.x * kChunk + 4 * threadIdx.x);
     uint64_t x = 0, total;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x += (uint64_t)(f[k].refs[i] == 0) | (uint64_t)(f[k].refs[i] > 0) << 32;
+    for (int i = 0; i < 4; ++i) x += (uint64_t)(f.refs[i] == 0) | (uint64_t)(f.refs[i] > 0) << 32;
     group_scan<kThreads>(x, total);
     if (threadIdx.x == 0) per_chunk[blockIdx.x] = make_int2((int)(uint32_t)total, (int)(total >> 32));
     return;
@@ -263,9 +243,24 @@ __global__ void __launch_bounds__(kPlanThreads) resize_plan_kernel(PagesView v, 
   }
 }
 
+// The last of grants [lo, hi) that begins at or before `rank`, where the first does.
+__device__ __forceinline__ int grant_of(const Grant* grants, int lo, int hi, int32_t rank) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (grants[mid].begin <= rank) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 // Each free page of a rank below plan.pages goes to the request whose share it
-// lies in.  Workgroups behind the chunks set the lengths.
+// lies in.  A chunk's pages have neighbouring ranks: its requests are looked up
+// once, and their shares lie in LDS (512 requests, a pool of half a million
+// pages: ASSIGN_US; a search in memory for each page 22 us).  Workgroups behind
+// the chunks set the lengths.
+constexpr int kShares = 2048;
 __global__ void __launch_bounds__(kThreads) resize_assign_kernel(PagesView v, const int32_t* want, Space s, int chunks, int32_t* copies) {
+  __shared__ Grant shares[kShares];
+  __shared__ int ends[2];
   const Plan plan = *s.plan;
   if ((int)blockIdx.x >= chunks) {
     const int64_t r = ((int64_t)blockIdx.x - chunks) * kThreads + threadIdx.x;
@@ -276,41 +271,41 @@ __global__ void __launch_bounds__(kThreads) resize_assign_kernel(PagesView v, co
   }
   const int32_t first = s.per_chunk[blockIdx.x].x;
   if (first >= plan.pages) return;
-  const int64_t base = (int64_t)blockIdx.x * kChunk;
-  Four f[4];
-  load_chunk(v, base, f);
-  int32_t before[4], total;
-  chunk_ranks(f, IsFree(), before, total);
+  const int64_t base = (int64_t)blockIdx.x * kChunk + 4 * threadIdx.x;
+  const Four f = load_four(v, base);
+  int32_t total, rank = first + chunk_ranks(f, IsFree(), total);
+  if (total == 0) return;
+  if (threadIdx.x < 2)
+    ends[threadIdx.x] = grant_of(s.grants, 0, v.n_req, threadIdx.x ? min(first + total, plan.pages) - 1 : first);
+  __syncthreads();
+  const int r0 = ends[0], n = ends[1] - r0 + 1;
+  const bool held = n <= kShares;
+  if (held) {
+    for (int i = threadIdx.x; i < n; i += kThreads) shares[i] = s.grants[r0 + i];
+    __syncthreads();
+  }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int32_t rank = first + before[k];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (f[k].refs[i] != 0) continue;
-      if (rank >= plan.pages) continue;
-      const int32_t page = (int32_t)(base + k * (4 * kThreads) + 4 * threadIdx.x + i);
-      int lo = 0, hi = v.n_req;                   // the last request that begins at or before this rank
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.grants[mid].begin <= rank) lo = mid; else hi = mid;
+  for (int i = 0; i < 4; ++i) {
+    if (f.refs[i] != 0) continue;
+    if (rank >= plan.pages) continue;
+    const int32_t page = (int32_t)(base + i);
+    const int r = held ? r0 + grant_of(shares, 0, n, rank) : grant_of(s.grants, r0, r0 + n, rank);
+    const Grant g = held ? shares[r - r0] : s.grants[r];
+    int32_t* row = v.table + r * v.table_stride;
+    int32_t at = rank - g.begin;
+    if (g.copy >= 0) {
+      if (at == 0) {
+        const int32_t old = row[g.has - 1];
+        row[g.has - 1] = page;
+        copies[2 * (int64_t)g.copy] = old;
+        copies[2 * (int64_t)g.copy + 1] = page;
+        atomicSub(v.refs + old, 1);
       }
-      const Grant g = s.grants[lo];
-      int32_t* row = v.table + lo * v.table_stride;
-      int32_t at = rank - g.begin;
-      if (g.copy >= 0) {
-        if (at == 0) {
-          const int32_t old = row[g.has - 1];
-          row[g.has - 1] = page;
-          copies[2 * (int64_t)g.copy] = old;
-          copies[2 * (int64_t)g.copy + 1] = page;
-          atomicSub(v.refs + old, 1);
-        }
-        --at;
-      }
-      if (at >= 0) row[g.has + at] = page;
-      v.refs[page] = 1;
-      ++rank;
+      --at;
     }
+    if (at >= 0) row[g.has + at] = page;
+    v.refs[page] = 1;
+    ++rank;
   }
 }
 
@@ -374,28 +369,21 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Space s, int
 __global__ void __launch_bounds__(kThreads) compact_list_kernel(PagesView v, Space s, int chunks, int32_t max_moves, int32_t* page_map) {
   const int2 first = s.per_chunk[blockIdx.x], pool = s.per_chunk[chunks];
   const int32_t most = min(max_moves, min(pool.x, pool.y));
-  const int64_t base = (int64_t)blockIdx.x * kChunk;
-  Four f[4];
-  load_chunk(v, base, f);
-  int32_t free_before[4], held_before[4], total;
-  chunk_ranks(f, IsFree(), free_before, total);
-  chunk_ranks(f, IsHeld(), held_before, total);
+  const int64_t base = (int64_t)blockIdx.x * kChunk + 4 * threadIdx.x;
+  const Four f = load_four(v, base);
+  int32_t total;
+  int32_t up = first.x + chunk_ranks(f, IsFree(), total), down = pool.y - 1 - (first.y + chunk_ranks(f, IsHeld(), total));
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int32_t up = first.x + free_before[k], down = pool.y - 1 - (first.y + held_before[k]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t page = base + k * (4 * kThreads) + 4 * threadIdx.x + i;
-      if (page >= v.n_pages) continue;
-      const int32_t refs = f[k].refs[i];
-      page_map[page] = refs == 0 ? -1 : (int32_t)page;
-      if (refs == 0) {
-        if (up < most) s.moves[up].y = (int32_t)page;
-        ++up;
-      } else if (refs > 0) {
-        if (down < most) s.moves[down].x = (int32_t)page;
-        --down;
-      }
+  for (int i = 0; i < 4; ++i) {
+    const int64_t page = base + i;
+    if (page >= v.n_pages) continue;
+    page_map[page] = f.refs[i] == 0 ? -1 : (int32_t)page;
+    if (f.refs[i] == 0) {
+      if (up < most) s.moves[up].y = (int32_t)page;
+      ++up;
+    } else if (f.refs[i] > 0) {
+      if (down < most) s.moves[down].x = (int32_t)page;
+      --down;
     }
   }
 }
@@ -430,6 +418,205 @@ __global__ void __launch_bounds__(kThreads) compact_tables_kernel(PagesView v, c
     if (!v.in_pool(page)) continue;
     const int32_t to = page_map[page];
     if (to >= 0 && to != page) row[j] = to;
+  }
+}
+
+// --- small pools and tables: a call is one workgroup, whose steps are apart by
+// barriers instead of launches ---
+
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallPages = 8192;                 // counts, claims and free pages lie in LDS
+constexpr int kSmallRequests = kSmallThreads;     // one thread each
+constexpr int64_t kSmallEntries = 32768;          // of all tables: 32 to a thread; in LDS for fork
+
+// This thread's pages are [lo, hi): neighbours, so that sums along the
+// workgroup are ranks.
+struct Own {
+  int lo, hi;
+};
+__device__ __forceinline__ Own own_pages(const PagesView& v) {
+  const int each = (v.n_pages + kSmallThreads - 1) / kSmallThreads;
+  return Own{min((int)threadIdx.x * each, v.n_pages), min(((int)threadIdx.x + 1) * each, v.n_pages)};
+}
+
+__global__ void __launch_bounds__(kSmallThreads) small_resize_kernel(PagesView v, const int32_t* want, int32_t* copies, int32_t* counts) {
+  extern __shared__ int32_t small_lds[];
+  int32_t* refs = small_lds;
+  int32_t* growing = refs + v.n_pages;            // requests that grow into the page
+  int32_t* first = growing + v.n_pages;           // the first of them; then the free pages in order
+  __shared__ int32_t has[kSmallRequests], needs[kSmallRequests], begin[kSmallRequests];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n_waves = kSmallThreads / 64;
+  Change c{-1, 0, false};
+  if (tid < v.n_req) c = change_of(v, want, tid);
+  has[tid] = c.has;
+  needs[tid] = c.needs;
+  for (int p = tid; p < v.n_pages; p += kSmallThreads) {
+    refs[p] = v.refs[p];
+    growing[p] = 0;
+    first[p] = 0x7fffffff;
+  }
+  __syncthreads();
+  for (int r = wave; r < v.n_req; r += n_waves) {
+    if (has[r] < 0) continue;
+    int32_t* row = v.table + r * v.table_stride;
+    for (int j = needs[r] + lane; j < has[r]; j += 64) {
+      const int32_t page = row[j];
+      if (v.in_pool(page)) atomicSub(refs + page, 1);
+      row[j] = -1;
+    }
+  }
+  int32_t last = -1;                              // the request's partly filled last page
+  if (c.part) {
+    last = v.table[tid * v.table_stride + c.has - 1];
+    if (v.in_pool(last)) {
+      atomicAdd(growing + last, 1);
+      atomicMin(first + last, tid);
+    } else {
+      last = -1;
+    }
+  }
+  __syncthreads();
+  const bool copy = last >= 0 && refs[last] > 1 && !(growing[last] == refs[last] && first[last] == tid);
+  const uint64_t more = (uint64_t)(c.has >= 0 && c.needs > c.has ? c.needs - c.has : 0) + copy;
+  const Own own = own_pages(v);
+  uint64_t n_free = 0;
+  for (int p = own.lo; p < own.hi; ++p) n_free += refs[p] == 0;
+  uint64_t free_all, all;
+  uint64_t rank = group_scan<kSmallThreads>(n_free, free_all);
+  const uint64_t before = group_scan<kSmallThreads>(more | (uint64_t)copy << 52, all);   // the claims have been read by now
+  const uint64_t pages = all & ((1ull << 52) - 1);
+  const bool enough = pages <= free_all;
+  if (tid == 0) {
+    counts[0] = enough ? (int32_t)(all >> 52) : 0;
+    counts[1] = enough ? 0 : (int32_t)min(pages - free_all, (uint64_t)0x7fffffff);
+  }
+  if (enough) {
+    for (int p = own.lo; p < own.hi; ++p)
+      if (refs[p] == 0) first[rank++] = p;
+    begin[tid] = (int32_t)(before & 0xffffffffu) + copy;
+  }
+  __syncthreads();
+  if (enough) {
+    if (copy) {
+      const int32_t page = first[begin[tid] - 1];
+      const int64_t i = (int64_t)(before >> 52);
+      copies[2 * i] = last;
+      copies[2 * i + 1] = page;
+      v.table[tid * v.table_stride + c.has - 1] = page;
+      atomicSub(refs + last, 1);
+      refs[page] = 1;
+    }
+    for (int r = wave; r < v.n_req; r += n_waves) {
+      if (has[r] < 0) continue;
+      int32_t* row = v.table + r * v.table_stride;
+      for (int j = has[r] + lane; j < needs[r]; j += 64) {
+        const int32_t page = first[begin[r] + j - has[r]];
+        row[j] = page;
+        refs[page] = 1;
+      }
+    }
+  }
+  if (c.has >= 0) {
+    const int32_t to = want[tid];
+    if (enough || to < v.lens[tid]) v.lens[tid] = to;
+  }
+  __syncthreads();
+  for (int p = tid; p < v.n_pages; p += kSmallThreads) v.refs[p] = refs[p];
+}
+
+__global__ void __launch_bounds__(kSmallThreads) small_fork_kernel(PagesView v, const int32_t* parents) {
+  extern __shared__ int32_t small_lds[];          // the tables as they were
+  __shared__ int32_t lens[kSmallRequests];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n_waves = kSmallThreads / 64;
+  if (tid < v.n_req) lens[tid] = v.lens[tid];
+  __syncthreads();
+  for (int r = wave; r < v.n_req; r += n_waves) {
+    const int32_t has = v.entries(lens[r]);
+    const int32_t* row = v.table + r * v.table_stride;
+    for (int j = lane; j < has; j += 64) small_lds[r * v.table_width + j] = row[j];
+  }
+  __syncthreads();
+  for (int r = wave; r < v.n_req; r += n_waves) {
+    const int from = fork_source(v, parents, lens, r);
+    if (from == r) continue;
+    const int32_t has = max(v.entries(lens[r]), 0), needs = from < 0 ? 0 : v.entries(lens[from]);
+    int32_t* row = v.table + r * v.table_stride;
+    for (int j = lane; j < max(has, needs); j += 64) {
+      const int32_t old = j < has ? small_lds[r * v.table_width + j] : -1;
+      const int32_t now = j < needs ? small_lds[from * v.table_width + j] : -1;
+      if (old != now || j >= has) {
+        if (v.in_pool(old)) atomicSub(v.refs + old, 1);
+        if (v.in_pool(now)) atomicAdd(v.refs + now, 1);
+        row[j] = now;
+      }
+    }
+    if (lane == 0) v.lens[r] = from < 0 ? 0 : lens[from];
+  }
+}
+
+__global__ void __launch_bounds__(kSmallThreads) small_compact_kernel(PagesView v, int32_t max_moves, int32_t* page_map, int32_t* copies,
+                                                                      int32_t* counts) {
+  extern __shared__ int32_t small_lds[];
+  int32_t* refs = small_lds;
+  int32_t* sources = refs + v.n_pages;            // held pages from the top; then the map
+  int32_t* targets = sources + v.n_pages;         // free pages from the bottom
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n_waves = kSmallThreads / 64;
+  for (int p = tid; p < v.n_pages; p += kSmallThreads) refs[p] = v.refs[p];
+  __syncthreads();
+  const Own own = own_pages(v);
+  uint64_t x = 0, all;                            // free pages, and held ones above
+  for (int p = own.lo; p < own.hi; ++p) x += (uint64_t)(refs[p] == 0) | (uint64_t)(refs[p] > 0) << 32;
+  const uint64_t before = group_scan<kSmallThreads>(x, all);
+  const int n_free = (int)(uint32_t)all, n_held = (int)(all >> 32), most = min(max_moves, min(n_free, n_held));
+  int up = (int)(uint32_t)before, down = n_held - 1 - (int)(before >> 32);
+  for (int p = own.lo; p < own.hi; ++p) {
+    if (refs[p] == 0) targets[up++] = p;
+    else if (refs[p] > 0) sources[down--] = p;
+  }
+  __syncthreads();
+  // sources fall and targets rise: the pairs that move come first
+  int from[kSmallPages / 2 / kSmallThreads], to[kSmallPages / 2 / kSmallThreads], moves = 0;
+#pragma unroll
+  for (int k = 0; k < kSmallPages / 2 / kSmallThreads; ++k) {
+    const int i = k * kSmallThreads + tid;
+    from[k] = to[k] = -1;
+    if (i < most && sources[i] > targets[i]) {
+      from[k] = sources[i];
+      to[k] = targets[i];
+      ++moves;
+      copies[2 * i] = from[k];
+      copies[2 * i + 1] = to[k];
+    }
+  }
+  uint64_t n_moves;
+  group_scan<kSmallThreads>((uint64_t)moves, n_moves);   // and the lists have been read by now
+  if (tid == 0) {
+    counts[0] = (int32_t)n_moves;
+    counts[1] = n_held;
+  }
+  int32_t* map = sources;
+  for (int p = tid; p < v.n_pages; p += kSmallThreads) map[p] = refs[p] == 0 ? -1 : p;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSmallPages / 2 / kSmallThreads; ++k) {
+    if (from[k] < 0) continue;
+    map[from[k]] = to[k];
+    refs[to[k]] = refs[from[k]];
+    refs[from[k]] = 0;
+  }
+  __syncthreads();
+  for (int p = tid; p < v.n_pages; p += kSmallThreads) {
+    page_map[p] = map[p];
+    v.refs[p] = refs[p];
+  }
+  for (int r = wave; r < v.n_req; r += n_waves) {
+    const int32_t has = v.entries(v.lens[r]);
+    int32_t* row = v.table + r * v.table_stride;
+    for (int j = lane; j < has; j += 64) {
+      const int32_t page = row[j];
+      if (!v.in_pool(page)) continue;
+      if (map[page] >= 0 && map[page] != page) row[j] = map[page];
+    }
   }
 }
 
@@ -487,6 +674,13 @@ int parts_of(const PagesView& v) {
   const int by_width = (int)(((int64_t)v.table_width + kThreads - 1) / kThreads), by_req = std::max(1, 1024 / std::max(1, v.n_req));
   return std::min(by_width, by_req);
 }
+// One launch where one workgroup is enough: beams of 4 x 8 requests, resize
+// SMALL_RESIZE us and the steps apart MANY_RESIZE.
+bool small_tables(const PagesView& v) {
+  return v.n_req <= kSmallRequests && (int64_t)v.n_req * v.table_width <= kSmallEntries;
+}
+bool small_pool(const PagesView& v) { return v.n_pages <= kSmallPages && small_tables(v); }
+size_t small_bytes(const PagesView& v) { return (size_t)v.n_pages * 12; }
 unsigned request_groups(const PagesView& v) { return (unsigned)((v.n_req + kThreads - 1) / kThreads); }
 
 }  // namespace
@@ -497,6 +691,10 @@ size_t kv_pages_workspace(int64_t n_pages, int32_t n_req, int32_t table_width) {
 
 hipError_t launch_kv_resize(const PagesView& v, const int32_t* want, int32_t* copies, int32_t* counts, void* workspace,
                             hipStream_t stream) {
+  if (small_pool(v)) {
+    small_resize_kernel<<<1, kSmallThreads, small_bytes(v), stream>>>(v, want, copies, counts);
+    return hipGetLastError();
+  }
   const Space s(workspace, v.n_pages, v.n_req, v.table_width);
   const int chunks = (int)chunks_of(v.n_pages), parts = parts_of(v);
   const unsigned groups = request_groups(v);
@@ -514,6 +712,10 @@ hipError_t launch_kv_resize(const PagesView& v, const int32_t* want, int32_t* co
 }
 
 hipError_t launch_kv_fork(const PagesView& v, const int32_t* parents, void* workspace, hipStream_t stream) {
+  if (small_tables(v)) {
+    small_fork_kernel<<<1, kSmallThreads, (size_t)v.n_req * v.table_width * 4, stream>>>(v, parents);
+    return hipGetLastError();
+  }
   const Space s(workspace, v.n_pages, v.n_req, v.table_width);
   const int parts = parts_of(v);
   fork_save_kernel<<<(unsigned)v.n_req * parts, kThreads, 0, stream>>>(v, parents, s, parts);
@@ -525,9 +727,13 @@ hipError_t launch_kv_fork(const PagesView& v, const int32_t* parents, void* work
 
 hipError_t launch_kv_compact(const PagesView& v, int32_t* page_map, int32_t* copies, int64_t max_copies,
                              int32_t* counts, void* workspace, hipStream_t stream) {
+  const int32_t max_moves = (int32_t)std::min<int64_t>(max_copies, v.n_pages / 2);
+  if (small_pool(v)) {
+    small_compact_kernel<<<1, kSmallThreads, small_bytes(v), stream>>>(v, max_moves, page_map, copies, counts);
+    return hipGetLastError();
+  }
   const Space s(workspace, v.n_pages, v.n_req, v.table_width);
   const int chunks = (int)chunks_of(v.n_pages);
-  const int32_t max_moves = (int32_t)std::min<int64_t>(max_copies, v.n_pages / 2);
   count_kernel<<<chunks, kThreads, 0, stream>>>(v, nullptr, nullptr, s.per_chunk, chunks);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

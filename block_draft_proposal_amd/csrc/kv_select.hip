@@ -5,8 +5,8 @@
 // bounds [2 D, blocks] by v_mfma_i32_16x16x64_i8, Q' holding the negative part
 // of a row's codes against the least keys and the positive part against the
 // greatest.  The largest of the group's heads becomes an order-preserving key in
-// the workspace.  The second takes each (row, kv head)'s n_take largest keys:
-// the threshold digit by digit from a histogram in LDS, then the blocks in order.
+// the workspace.  The second takes each (row, kv head)'s n_take largest keys: it
+// finds the threshold by halving their range, then the blocks in order.
 #include <algorithm>
 
 #include "kv_sparse.h"
@@ -29,7 +29,9 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
   extern __shared__ __align__(16) int8_t queries[];   // [steps][kOps][64 lanes] x 16 bytes: the operands as they lie
   const KvView& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = per_group.d;
-  // consecutive workgroups take the kv heads of the same blocks
+  // Consecutive workgroups, on as many XCDs, take the kv heads of the same
+  // blocks.  (The heads on one XCD, so that a line of scale bytes is fetched
+  // once: one row of 8192 blocks 18 us, this way 9; 512 rows of 2048 38 and 41.)
   const int head = blockIdx.x % c.n_kv_heads;
   const int rest = blockIdx.x / c.n_kv_heads, chunk = rest % chunks;
   const int64_t row0 = (int64_t)(rest / chunks) * NT;
@@ -88,14 +90,20 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
     const int32_t blocks = kv_blocks(c, c.start[req]);
     const int32_t* table = c.table + req * c.table_stride;
     const int32_t to = (int32_t)min((int64_t)blocks, ((int64_t)chunk + 1) * chunk_blocks);
-    for (int64_t b0 = (int64_t)chunk * chunk_blocks + wave * kWaveBlocks; b0 < to; b0 += kStepBlocks) {
+    int32_t ids[4];                               // pages of the step, looked up a step ahead
+    auto look_up = [&](int64_t b0) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ids[t] = table[(int32_t)min(b0 + 16 * t + (lane & 15), (int64_t)blocks - 1)];
+    };
+    int64_t b0 = (int64_t)chunk * chunk_blocks + wave * kWaveBlocks;
+    if (b0 < to) look_up(b0);
+    for (; b0 < to; b0 += kStepBlocks) {
       i32x4_t edge[4][kOps];
       uint32_t byte[4];
       bool broken[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int32_t b = (int32_t)min(b0 + 16 * t + (lane & 15), (int64_t)blocks - 1);
-        int32_t id = table[b];
+        int32_t id = ids[t];
         broken[t] = id < 0 || id >= c.n_pages;
         if (broken[t]) id = 0;
         const int64_t at = (int64_t)id * c.n_kv_heads + head;
@@ -104,6 +112,7 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
         for (int o = 0; o < kOps; ++o) edge[t][o] = *reinterpret_cast<const i32x4_t*>(p + 64 * o);
         byte[t] = a.scale[at];
       }
+      if (b0 + kStepBlocks < to) look_up(b0 + kStepBlocks);
       int best[4][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -161,113 +170,220 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
 
 // --- the choice ---
 
-constexpr int kDigits = 2048;                     // bins: digits of 11, 11 and 10 bits from the top
-constexpr int kOwn = 16;                          // keys of a thread in a segment, neighbours
-constexpr int kSegment = kOwn * kThreads;
-
-__device__ __forceinline__ uint32_t digit(uint32_t key, int pass) {
-  return pass == 0 ? key >> 21 : pass == 1 ? (key >> 10) & 2047u : key & 1023u;
-}
-__device__ __forceinline__ uint32_t prefix_mask(int pass) { return pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u; }
-
-// The thread's keys of the segment at s0; `n` of them are there.
-__device__ __forceinline__ int load_keys(const uint32_t* keys, int64_t s0, int32_t blocks, uint32_t (&k)[kOwn]) {
-  const int64_t at = s0 + (int64_t)threadIdx.x * kOwn;
-  const int n = (int)max((int64_t)0, min((int64_t)kOwn, blocks - at));
+// The thread's keys of the segment at s0; 0 past the last, which no key is.
+template <int T, int kOwn>
+__device__ __forceinline__ void load_keys(const uint32_t* keys, int tid, int64_t s0, int32_t blocks, uint32_t (&k)[kOwn]) {
+  const int64_t at = s0 + (int64_t)tid * kOwn;
+  typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+  if (at + kOwn <= blocks) {
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) k[i] = i < n ? keys[at + i] : 0u;
-  return n;
-}
-
-// Exclusive sums of two 16-bit counts along the workgroup, and the totals.
-__device__ __forceinline__ uint32_t scan_counts(uint32_t x, uint32_t& total, uint32_t* sums) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t scan = x;
+    for (int i = 0; i < kOwn / 4; ++i) {
+      const u32x4_a4 x = *reinterpret_cast<const u32x4_a4*>(keys + at + 4 * i);
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t y = (uint32_t)__shfl_up((int)scan, o, 64);
-    if (lane >= o) scan += y;
+      for (int j = 0; j < 4; ++j) k[4 * i + j] = x[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) k[i] = at + i < blocks ? keys[at + i] : 0u;
   }
-  __syncthreads();
-  if (lane == 63) sums[wave] = scan;
-  __syncthreads();
-  uint32_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) {
-    if (i < wave) before += sums[i];
-    total += sums[i];
-  }
-  return before + scan - x;
 }
 
-__global__ void __launch_bounds__(kThreads) select_take_kernel(SelectArgs a) {
-  __shared__ uint32_t bins[kDigits];
-  __shared__ uint32_t sums[kThreads / 64];
-  __shared__ uint32_t found[2];
+// x of all waves, summed; `at` alternates between calls, so that one barrier is
+// enough.
+template <int T>
+__device__ __forceinline__ uint32_t all_waves(uint32_t x, uint32_t (*sums)[T / 64], int& at) {
+  at ^= 1;
+  if ((threadIdx.x & 63) == 0) sums[at][threadIdx.x >> 6] = x;
+  __syncthreads();
+  uint32_t all = 0;
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) all += sums[at][i];
+  return all;
+}
+
+// The score that a key stands for.
+__device__ __forceinline__ float key_score(uint32_t key) { return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key); }
+
+// T threads for a (row, kv head), kOwn neighbouring keys each.
+//
+// The threshold is the smallest key that is taken.  A histogram of the scores
+// between the least and the greatest leaves one bin that it lies in, and where
+// few keys share it they are ranked one by one; else the bin is the next range.
+// Bins are even in the score, not in the key's bits: scores of one magnitude
+// share their upper bits, and all threads adding to one bin would wait in line
+// (one row of 8192 blocks: 11 bits of the key at a time 29 us, so TAKE_1).
+template <int T, int kOwn>
+__global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
+  constexpr int kSegment = kOwn * T, kBins = 8 * T < 2048 ? 8 * T : 2048, kEach = kBins / T, kFew = 64;
+  __shared__ uint32_t bins[kBins];
+  __shared__ uint32_t sums[2][T / 64], lows[T / 64], highs[T / 64];
+  __shared__ uint32_t few[kFew];
+  __shared__ uint32_t found[3], n_few, range[2];
   const KvView& c = a.c;
-  const int64_t row = blockIdx.x / c.n_kv_heads;
-  const int head = blockIdx.x - (unsigned)row * c.n_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t row = blockIdx.x / (unsigned)c.n_kv_heads;
   int32_t req = 0;
   int64_t pos = 0;
   if (!kv_row_position(c, row, row, req, pos) || row - c.offsets[req] >= a.max_nodes) return;   // the same in every thread
   const int32_t blocks = kv_blocks(c, c.start[req]), take = a.n_take;
-  int32_t* out = a.out + ((int64_t)row * c.n_kv_heads + head) * take;
+  int32_t* out = a.out + (int64_t)blockIdx.x * take;
   if (blocks <= take) {
-    for (int i = threadIdx.x; i < take; i += kThreads) out[i] = i < blocks ? i : -1;
+    for (int i = tid; i < take; i += T) out[i] = i < blocks ? i : -1;
     return;
   }
-  const uint32_t* keys = a.keys + ((int64_t)row * c.n_kv_heads + head) * c.table_width;
+  const uint32_t* keys = a.keys + (int64_t)blockIdx.x * c.table_width;
+  const bool held = blocks <= kSegment;           // the keys stay in registers
   uint32_t k[kOwn];
-  int n = load_keys(keys, 0, blocks, k);
-  // the threshold: the take-th largest key, a digit at a time from the top
-  uint32_t threshold = 0, left = (uint32_t)take;  // keys still to be taken among those that agree so far
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    for (int i = threadIdx.x; i < kDigits; i += kThreads) bins[i] = 0;
-    __syncthreads();
+  load_keys<T, kOwn>(keys, tid, 0, blocks, k);
+  int at_sum = 0;
+  // calls f for every key (and for the zeros past the last)
+  auto for_keys = [&](auto f) {
     for (int64_t s0 = 0; s0 < blocks; s0 += kSegment) {
-      if (blocks > kSegment) n = load_keys(keys, s0, blocks, k);
+      if (!held) load_keys<T, kOwn>(keys, tid, s0, blocks, k);
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-        if (i < n && ((k[i] ^ threshold) & prefix_mask(pass)) == 0) atomicAdd(&bins[digit(k[i], pass)], 1u);
+      for (int i = 0; i < kOwn; ++i) f(k[i]);
     }
-    __syncthreads();
-    // thread t holds bins 2047 - 8 t down to 2040 - 8 t
-    uint32_t own[8], sum = 0, total;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      own[i] = bins[kDigits - 1 - (int)threadIdx.x * 8 - i];
-      sum += own[i];
-    }
-    uint32_t above = scan_counts(sum, total, sums);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (above < left && above + own[i] >= left) {
-        found[0] = kDigits - 1 - threadIdx.x * 8 - i;
-        found[1] = left - above;
-      }
-      above += own[i];
-    }
-    __syncthreads();
-    threshold |= found[0] << (pass == 0 ? 21 : pass == 1 ? 10 : 0);
-    left = found[1];
+  };
+
+  for (int i = tid; i < kBins; i += T) bins[i] = 0;
+  if (tid == 0) n_few = 0;
+  uint32_t low = 0xffffffffu, high = 0, forced = 0, broken = 0;
+  for_keys([&](uint32_t key) {
+    const bool plain = key - 1u < kBroken - 1u;
+    low = min(low, plain ? key : 0xffffffffu);
+    high = max(high, plain ? key : 0u);
+    forced += key == kForced;
+    broken += key == kBroken;
+  });
+  low = ~wave_max_u32(~low);
+  high = wave_max_u32(high);
+  if (lane == 0) {
+    lows[wave] = low;
+    highs[wave] = high;
   }
+  // 2^24 blocks at most over at least 256 threads: both counts fit a word of 64 bits' halves in turn
+  forced = all_waves<T>(wave_sum_u32(forced), sums, at_sum);
+  broken = all_waves<T>(wave_sum_u32(broken), sums, at_sum);
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) {
+    low = min(low, lows[i]);
+    high = max(high, highs[i]);
+  }
+  uint32_t threshold = low, left = (uint32_t)take;  // left: keys at the threshold that are taken, the first ones
+  if (forced >= left) {
+    threshold = kForced;
+  } else if (forced + broken >= left) {
+    threshold = kBroken;
+    left -= forced;
+  } else {
+    left -= forced + broken;                      // of more keys in [low, high]
+#pragma unroll 1
+    while (low < high) {
+      // the least key is in the first bin and the greatest in the last, and a
+      // greater score never in a lower bin
+      const float least = key_score(low), span = key_score(high) - least;
+      auto bin_of = [&](uint32_t key) { return (int)((key_score(key) - least) / span * (float)(kBins - 1)); };
+      for_keys([&](uint32_t key) {
+        if (key >= low && key <= high) atomicAdd(&bins[bin_of(key)], 1u);
+      });
+      __syncthreads();
+      uint32_t own[kEach], sum = 0;               // thread t holds the bins from the top down
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        own[i] = bins[kBins - 1 - tid * kEach - i];
+        sum += own[i];
+      }
+      uint32_t scan = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = (uint32_t)__shfl_up((int)scan, o, 64);
+        if (lane >= o) scan += y;
+      }
+      at_sum ^= 1;
+      if (lane == 63) sums[at_sum][wave] = scan;
+      __syncthreads();
+      uint32_t above = scan - sum;
+#pragma unroll
+      for (int i = 0; i < T / 64; ++i)
+        if (i < wave) above += sums[at_sum][i];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (above < left && above + own[i] >= left) {
+          found[0] = kBins - 1 - tid * kEach - i;
+          found[1] = left - above;
+          found[2] = own[i];
+        }
+        above += own[i];
+        bins[kBins - 1 - tid * kEach - i] = 0;    // for the next round
+      }
+      if (tid == 0) {
+        range[0] = 0xffffffffu;
+        range[1] = 0;
+      }
+      __syncthreads();
+      const int bin = (int)found[0];
+      const uint32_t in_bin = found[2], from = low, to = high;
+      left = found[1];
+      if (in_bin <= kFew) {
+        for_keys([&](uint32_t key) {
+          if (key >= from && key <= to && bin_of(key) == bin) few[atomicAdd(&n_few, 1u)] = key;
+        });
+        __syncthreads();
+        const uint32_t mine = few[min((uint32_t)lane, in_bin - 1)];
+        uint32_t greater = 0, as_great = 0;
+        for (uint32_t i = 0; i < in_bin; ++i) {
+          const uint32_t other = few[i];
+          greater += other > mine;
+          as_great += other >= mine;
+        }
+        const uint64_t hit = __ballot(greater < left && as_great >= left);
+        const int first = __builtin_ctzll(hit);
+        threshold = (uint32_t)__builtin_amdgcn_readlane((int)mine, first);
+        left -= (uint32_t)__builtin_amdgcn_readlane((int)greater, first);
+        break;
+      }
+      low = 0xffffffffu;
+      high = 0;
+      for_keys([&](uint32_t key) {
+        if (key < from || key > to || bin_of(key) != bin) return;
+        low = min(low, key);
+        high = max(high, key);
+      });
+      atomicMin(&range[0], low);
+      atomicMax(&range[1], high);
+      __syncthreads();
+      threshold = low = range[0];
+      high = range[1];
+    }
+  }
+
   // blocks above the threshold, and the first `left` at it, in order
   uint32_t base_above = 0, base_at = 0;
   for (int64_t s0 = 0; s0 < blocks; s0 += kSegment) {
-    if (blocks > kSegment) n = load_keys(keys, s0, blocks, k);
-    uint32_t x = 0, total;
+    if (!held) load_keys<T, kOwn>(keys, tid, s0, blocks, k);
+    uint32_t x = 0;                               // above in the lower half, at it in the upper
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (i < n) x += k[i] > threshold ? 1u : k[i] == threshold ? 0x10000u : 0u;
-    const uint32_t before = scan_counts(x, total, sums);
+    for (int i = 0; i < kOwn; ++i) x += k[i] > threshold ? 1u : k[i] == threshold ? 0x10000u : 0u;
+    uint32_t scan = x;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t y = (uint32_t)__shfl_up((int)scan, o, 64);
+      if (lane >= o) scan += y;
+    }
+    at_sum ^= 1;
+    if (lane == 63) sums[at_sum][wave] = scan;
+    __syncthreads();
+    uint32_t before = scan - x, total = 0;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) {
+      if (i < wave) before += sums[at_sum][i];
+      total += sums[at_sum][i];
+    }
     uint32_t above = base_above + (before & 0xffffu), at = base_at + (before >> 16);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-      if (i >= n) continue;
       const bool is_above = k[i] > threshold, is_at = k[i] == threshold;
-      if (is_above || (is_at && at < left)) out[above + min(at, left)] = (int32_t)(s0 + threadIdx.x * kOwn + i);
+      if (is_above || (is_at && at < left)) out[above + min(at, left)] = (int32_t)(s0 + tid * kOwn + i);
       above += is_above;
       at += is_at;
     }
@@ -315,7 +431,11 @@ hipError_t launch_kv_select(const SelectArgs& a, hipStream_t stream) {
                        : a.c.head_dim == 128 ? score_dim<128>(a, stream)
                                              : score_dim<256>(a, stream);
   if (e != hipSuccess) return e;
-  select_take_kernel<<<(unsigned)(a.c.n_rows * a.c.n_kv_heads), kThreads, 0, stream>>>(a);
+  // Threads of a (row, kv head): as few as hold the keys of the longest prefix.
+  const unsigned items = (unsigned)(a.c.n_rows * a.c.n_kv_heads);
+  if (a.c.table_width <= 8 * 256) select_take_kernel<256, 8><<<items, 256, 0, stream>>>(a);
+  else if (a.c.table_width <= 16 * 256) select_take_kernel<256, 16><<<items, 256, 0, stream>>>(a);
+  else select_take_kernel<1024, 8><<<items, 1024, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -71,7 +71,8 @@ def empty(n_pages, n, width, page, reserved=()):
 
 
 @pytest.mark.parametrize("seed,n_pages,n,width,page", [(0, 40, 6, 9, 4), (1, 300, 33, 20, 16), (2, 5000, 7, 900, 1), (3, 64, 1, 30, 20),
-                                                       (4, 9000, 300, 40, 7), (5, 12, 5, 3, 65536)])
+                                                       (4, 9000, 300, 40, 7), (5, 12, 5, 3, 65536),
+                                                       (6, 8300, 41, 900, 1), (7, 8192, 1024, 32, 16), (8, 8192, 1025, 3, 5), (9, 100, 3, 20000, 1)])
 def test_random_lives(seed, n_pages, n, width, page):
     require_gpu()
     say(f"random lives {seed}")

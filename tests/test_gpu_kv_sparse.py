@@ -98,6 +98,19 @@ def test_bounds_ignore_what_is_not_there():
     check_bounds(cache, tensors, table, host_table, [39, 0, 0, 8], [2147483647, 7, 0, 8])
 
 
+@pytest.mark.parametrize("n_req", [300, 2048, 2049])
+def test_bounds_of_many_requests(n_req):
+    """More requests than threads, and than the line holds; many with nothing to do."""
+    require_gpu()
+    say(f"bounds of {n_req}")
+    rng = np.random.default_rng(n_req)
+    page = 4
+    start = rng.integers(0, 9, n_req)
+    rows = np.where(rng.random(n_req) < 0.4, 0, rng.integers(0, 14, n_req))
+    cache, tensors, (table, _, _), host, _ = written("i8", start, rows, page, 2, 64)
+    check_bounds(cache, tensors, table, host[0], start, start + rows)
+
+
 # --- the choice ---
 
 
