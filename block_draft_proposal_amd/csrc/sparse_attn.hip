@@ -23,58 +23,13 @@
 // partial sums in a fixed order.
 #include <algorithm>
 
-#include "kv_mfma.h"
-#include "kv_sparse.h"
+#include "sparse_core.h"
 
 namespace dflash {
 namespace {
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-// Partials of one call at most, and so the workspace.
+// Partials of one call at most, and so their part of the workspace.
 constexpr int kMaxParts = 1024;
-
-template <int DT, int D, int GT>
-struct Shape {
-  static constexpr int kRB = D * (DT == DFLASH_BF16 ? 2 : 1);
-  static constexpr int kChunks = kRB / 16;
-  static constexpr int kWaves = kRB == 512 ? 2 : 4, kThreads = 64 * kWaves;
-  static constexpr int kTile = 32 * kRB;                              // K (or V) of a step
-  static constexpr int kLoads = kTile / 1024;                         // direct loads of K (or V) a lane
-  static constexpr int kWaveStages = 2 * 2 * kTile;
-  static constexpr int kRowsAt = kWaves * kWaveStages;                // [wave][4 steps][32] byte offsets, int64
-  static constexpr int kScalesAt = kRowsAt + kWaves * 4 * 32 * 8;     // [wave][4 steps][K 32, V 32] fp32
-  static constexpr int kLoop = kScalesAt + (DT == DFLASH_BF16 ? 0 : kWaves * 4 * 64 * 4);
-  static constexpr int kJoin = kWaves * 16 * (D + 2) * 4;             // after the loop: [wave] O, m and l of a tile
-  static constexpr int kLds = kLoop > kJoin ? kLoop : kJoin;
-  static_assert(kLds <= 160 * 1024 && 2 * kLoads < 63, "LDS of a CU, loads in flight");
-
-  // Chunk c of stage row r lies in slot c ^ swizzle(r), so that reads of one
-  // instruction fall on different banks: for K, 16 consecutive rows of one
-  // chunk; for V's transposed reads, 8 consecutive rows of two chunks (16-bit
-  // elements) or 8 and the 8 that are 16 further of one (8-bit).
-  static constexpr int kRowsPerBanks = kRB >= 256 ? 1 : 256 / kRB;
-  __device__ static __forceinline__ int k_swizzle(int r) { return (r / kRowsPerBanks) & (16 / kRowsPerBanks - 1); }
-  __device__ static __forceinline__ int v_swizzle(int r) {
-    constexpr int n = 8 / kRowsPerBanks;
-    if constexpr (DT == DFLASH_BF16) return ((r / kRowsPerBanks) & (n - 1)) << 1;
-    else return ((r / kRowsPerBanks) & (n - 1)) | (((r >> 4) & 1) * n);
-  }
-};
-
-// x of the lanes 16, 32 and 48 away, combined.
-__device__ __forceinline__ float quarter_max(float x) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
-}
-__device__ __forceinline__ float quarter_sum(float x) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
-}
-
-// Orders a wave's LDS accesses as they are written (the hardware keeps a
-// wave's in order).
-__device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
 
 // A row, a kv head and 16 GT of its group's heads.  Rows are neighbours.
 struct Item {
@@ -95,9 +50,9 @@ struct Part {                                     // what a split item leaves: [
 };
 
 template <int DT, int D, int GT>
-__global__ void __launch_bounds__((Shape<DT, D, GT>::kThreads), 1)
+__global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
     sparse_attention_kernel(SparseArgs a, int all_heads, int tiles, int splits) {
-  using S = Shape<DT, D, GT>;
+  using S = SparseShape<DT, D>;
   constexpr int kRB = S::kRB, kOps = D / 32, kBlocks = D / 16;
   extern __shared__ __align__(16) unsigned char sa_smem[];
   const KvView& c = a.c;
@@ -167,7 +122,7 @@ __global__ void __launch_bounds__((Shape<DT, D, GT>::kThreads), 1)
   bool bad = over, seen = over;
 
   // --- looking up: lanes 0 .. 31 and 32 .. 63 both hold the step's 32 keys ---
-  int32_t a_block = 0, a_off = 0, a_bit = 0, b_page = -1, b_off = 0;
+  int32_t a_block = 0, a_before = -1, a_off = 0, a_bit = 0, b_page = -1, b_off = 0;
   uint32_t a_word = 0, c_byte = 0, vis0 = 0, vis1 = 0, vis2 = 0, vis3 = 0;
   bool a_ok = false, a_chosen = false, b_ok = false, c_ok = false;
 
@@ -181,14 +136,18 @@ __global__ void __launch_bounds__((Shape<DT, D, GT>::kThreads), 1)
     a_block = d;
     a_word = ~0u;
     a_bit = 0;
-    if (a_ok && a_chosen) a_block = chosen[d];
+    a_before = -1;
+    if (a_ok && a_chosen) {
+      a_block = chosen[d];
+      if (d > 0) a_before = chosen[d - 1];
+    }
     if (mask && a_ok && !a_chosen && y >= tail) {
       a_word = mask[(y - tail) >> 5];
       a_bit = (y - tail) & 31;
     }
   };
   auto find_page = [&]() {
-    b_ok = a_ok && (!a_chosen || (a_block >= 0 && a_block < full)) && ((a_word >> a_bit) & 1u);
+    b_ok = a_ok && (!a_chosen || (a_block >= 0 && a_block < full && a_block > a_before)) && ((a_word >> a_bit) & 1u);
     b_off = a_off;
     b_page = -1;
     if (b_ok) b_page = table[a_block];             // within the table: start + n is
@@ -442,7 +401,7 @@ __global__ void __launch_bounds__(256) sparse_join_kernel(SparseArgs a, int all_
 
 template <int DT, int D, int GT>
 hipError_t run(const SparseArgs& a, hipStream_t s) {
-  using S = Shape<DT, D, GT>;
+  using S = SparseShape<DT, D>;
   const int group = a.n_q_heads / a.c.n_kv_heads, tiles = (group + 16 * GT - 1) / (16 * GT);
   const int64_t items = a.c.n_rows * a.c.n_kv_heads * tiles;
   // Workgroups to an item: as many as fill the chip twice, while each wave has
@@ -476,10 +435,13 @@ hipError_t run_dim(const SparseArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t sparse_attention_bytes(const KvView& c, int64_t n_rows, int32_t n_take, int32_t max_nodes, int32_t n_q_heads) {
-  return ((size_t)kMaxParts * Part::floats(n_q_heads / c.n_kv_heads, c.head_dim) * sizeof(float) + 255) / 256 * 256;
+  const size_t rows = ((size_t)kMaxParts * Part::floats(n_q_heads / c.n_kv_heads, c.head_dim) * sizeof(float) + 255) / 256 * 256;
+  return max_nodes == 1 ? rows : std::max(rows, sparse_tile_bytes(c, n_rows, n_take, n_q_heads));
 }
 
 hipError_t launch_sparse_attention(const SparseArgs& a, hipStream_t stream) {
+  const TilePlan plan = sparse_tile_plan(a.c, a.c.n_rows, a.n_take, a.max_nodes, a.n_q_heads);
+  if (plan.use) return launch_sparse_tiles(a, plan, stream);
   if (a.c.dtype == DFLASH_BF16) return run_dim<DFLASH_BF16>(a, stream);
   if (a.c.dtype == DFLASH_E4M3) return run_dim<DFLASH_E4M3>(a, stream);
   return run_dim<DFLASH_I8>(a, stream);

@@ -87,19 +87,24 @@ int dflash_kv_select(const dflash_page_bounds* bounds, const dflash_kv_batch* ba
  * blocks[i][g][0 .. n_take), the prefix's positions from B * page_size on, and
  * the nodes of its request that its mask names (mask NULL: a chain).  With all
  * blocks 0 .. B - 1 it is dflash_tree_attention.
- *   blocks  int32 [n_rows, n_kv_heads, n_take], 4-byte aligned.  Entries below 0
- *           or from B on name nothing; a block that is named twice counts
- *           twice.  n_take 0 .. 65536 (0: blocks is not looked at)
+ *   blocks  int32 [n_rows, n_kv_heads, n_take], 4-byte aligned, in ascending
+ *           order as dflash_kv_select leaves them: an entry below 0 or from B
+ *           on, or not above the entry before it, names nothing (so that a list
+ *           that falls and rises again may not name a block twice: it may then
+ *           count once or twice).  n_take 0 .. 65536 (0: blocks is not looked at)
  *   q, mask, out, max_nodes, scale   as for dflash_tree_attention
  * A row that sees nothing gets zeros.  What a row does not see has no effect on
- * it.  Positions without a page in the pool make the rows that see them NaN;
+ * it, whatever values the cache holds there, but for the last bits: the nodes of
+ * a request are taken together.  Positions without a page in the pool make the rows that see them NaN;
  * so do lengths beyond the table.
  * Arithmetic: as for dflash_tree_attention; an infinity or a NaN among the
  * values that a row sees makes its result an infinity or a NaN.  A call's
- * result is the same every time, and a row's does not depend on what other
- * rows of the batch hold, but for how n_rows and max_nodes split the sums.
- * Scratch: dflash_sparse_attention_workspace_size() bytes, 256-byte aligned
- * (none: 0); it may not overlap anything else of the call, and calls that may
+ * result is the same every time; its sums are split by the whole batch, so a
+ * request may differ in the last bits from one batch to another.
+ *   max_nodes also decides whether the nodes of a request are taken together:
+ *           give the batch's own largest number, 1 for plain decoding.
+ * Scratch: dflash_sparse_attention_workspace_size() bytes, 256-byte aligned; it
+ * never falls with n_rows, n_take, max_nodes or n_q_heads; it may not overlap anything else of the call, and calls that may
  * run at the same time need one each. */
 size_t dflash_sparse_attention_workspace_size(const dflash_kv_cache* cache, int64_t n_rows, int32_t n_take,
                                               int32_t max_nodes, int32_t n_q_heads);

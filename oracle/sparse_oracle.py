@@ -91,7 +91,8 @@ def sparse_attention(q, cache, table, start, offsets, blocks, mask, scale, out):
         for i in range(n):
             row = int(offsets[r]) + i
             for g in range(heads):
-                pos = [b * page_size + s for b in blocks[row, g] if 0 <= b < full for s in range(page_size)]
+                named = [b for before, b in zip([-1, *blocks[row, g][:-1]], blocks[row, g]) if 0 <= b < full and b > before]
+                pos = [b * page_size + s for b in named for s in range(page_size)]
                 pos += list(range(full * page_size, a))
                 pos += [a + j for j in range(n) if K.sees(mask, int(offsets[r]), i, j)]
                 if not pos:

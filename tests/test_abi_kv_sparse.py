@@ -115,5 +115,10 @@ def test_sparse_refusals():
     size = lambda **kw: S._fns().dflash_sparse_attention_workspace_size(  # noqa: E731
         _structs()[0], *({**dict(rows=8, take=3, nodes=4, hq=32), **kw}).values())
     assert size() > 0 and _sparse(n=size() - 1) == -3
-    assert size(rows=100000) == size(take=0) == size(nodes=4096) == size()
+    last = 0
+    for kw in (dict(nodes=1), dict(), dict(nodes=4096), dict(rows=9, nodes=4096), dict(rows=9, take=4), dict(rows=1000, take=4),
+               dict(rows=1 << 20, take=4), dict(rows=1 << 20, take=65536), dict(rows=1 << 20, take=65536, hq=512)):
+        assert size(**kw) >= last, kw
+        last = size(**kw)
+    assert size(take=0) > 0
     assert size(rows=0) == size(hq=12) == size(hq=8 * 65) == size(take=-1) == size(nodes=0) == size(nodes=4097) == size(rows=1 << 22) == 0

@@ -269,6 +269,12 @@ def check_sparse(cache, tensors, plan, host, n_rows, group, blocks, mask=None, s
     (128, 1, 40, 64, [500], [3], 6, "tree"),
     (256, 1, 64, 16, [130, 40], [2, 1], 7, None),
     (128, 1, 33, 33, [70, 3], [70, 1], 2, "random"),
+    (128, 1, 4, 16, [200, 77, 0], [70, 33, 64], 6, "tree"),
+    (64, 2, 1, 16, [300, 9], [40, 64], 9, "random"),
+    (128, 2, 8, 16, [300, 500, 31], [16, 10, 8], 9, None),
+    (256, 1, 4, 16, [300, 100], [16, 9], 9, "tree"),
+    (128, 2, 3, 16, [120], [5], 3, "full"),
+    (64, 1, 2, 1, [3000], [6], 500, "tree"),
 ])
 def test_sparse(kind, dim, heads, group, page, start, rows, take, shape):
     require_gpu()
@@ -279,14 +285,15 @@ def test_sparse(kind, dim, heads, group, page, start, rows, take, shape):
     check_sparse(cache, tensors, plan, host, n_rows, group, blocks, mask)
 
 
-@pytest.mark.parametrize("kind,n_req,rows", [("bf16", 1, 1), ("e4m3", 3, 4), ("i8", 40, 5), ("bf16", 150, 4)])
+@pytest.mark.parametrize("kind,n_req,rows", [("bf16", 1, 1), ("i8", 2, 1), ("e4m3", 3, 1), ("e4m3", 3, 4), ("bf16", 1, 7), ("i8", 2, 3), ("i8", 40, 5), ("bf16", 150, 4)])
 def test_sparse_splits(kind, n_req, rows):
     """From one item, split over many workgroups, to more than the chip holds."""
     require_gpu()
     say(f"splits {kind} {n_req}")
-    start = [400 + 13 * r if r % 3 else 40 * r for r in range(n_req)]
+    most = 1300 if n_req <= 3 else 400                   # up to 1040 keys: four workgroups to an item
+    start = [most - 13 * r if r % 3 == 0 else 40 * r for r in range(n_req)]
     cache, tensors, plan, host, n_rows = written(kind, start, [rows] * n_req, 16, 2, 64)
-    blocks = pick(host, n_rows, 2, 16, 24, 2)
+    blocks = pick(host, n_rows, 2, 16, 64 if n_req <= 3 else 24, 2, kind="all" if n_req <= 3 else "some")
     check_sparse(cache, tensors, plan, host, n_rows, 3, blocks)
 
 
@@ -315,7 +322,7 @@ def test_rows_that_see_nothing_and_blocks_that_name_nothing(kind):
     blocks = np.full((n_rows, heads, 4), -1, dtype=np.int32)
     blocks[3, 0] = [5, -7, 2, 2147483647]                # beyond the prefix's full pages
     blocks[4, 1] = [-1, -1, 0, -1]                       # a gap before an entry
-    blocks[5, 0] = [2, 0, 1, 0]                          # in any order, one of them twice
+    blocks[5, 0] = [2, 2, 0, 1]                          # not above the entry before: named once, and not at all
     mask = np.zeros((n_rows, 1), dtype=np.uint64)
     mask[1, 0] = 0b100
     mask[5, 0] = 0xfffffffffffffff0                       # bits past the nodes
@@ -323,37 +330,71 @@ def test_rows_that_see_nothing_and_blocks_that_name_nothing(kind):
     check_sparse(cache, tensors, plan, host, n_rows, 4, blocks[:, :, :0], mask)
 
 
-@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-def test_what_is_not_seen_has_no_effect(kind):
-    """NaN and infinities in blocks that are not chosen, in nodes that are not
-    seen and behind the end."""
+@pytest.mark.parametrize("rows", [[4, 6], [1, 1]])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
+@pytest.mark.parametrize("start", [[50, 20], [900, 700]])
+def test_what_is_not_seen_has_no_effect(kind, rows, start):
+    """Every row in turn, with NaN in all blocks that it has not chosen and in
+    all nodes that it does not see, which other rows of its request do see."""
     require_gpu()
-    say(f"unseen {kind}")
+    say(f"unseen {kind} {rows} {start}")
     page, heads, dim = 8, 2, 128
-    cache, tensors, plan, host, n_rows = written(kind, [50, 20], [4, 6], page, heads, dim)
-    blocks = pick(host, n_rows, heads, page, 3, 5)
+    cache, tensors, plan, host, n_rows = written(kind, start, rows, page, heads, dim)
+    blocks = pick(host, n_rows, heads, page, max(start) // page // 3, 5)
     mask = tree_mask(n_rows, host[2], 1)
     q, out, kw = check_sparse(cache, tensors, plan, host, n_rows, 4, blocks, mask)
+    clean = oracle_cache(*tensors)
+    want = np.full(tuple(out.shape), 7.0)
+    spread, reach = S.sparse_attention(codes_f64(q), clean, *host, blocks, mask, dim ** -0.5, want)
+    bound = attention_bound(want, spread, reach, dim)
+    names = ("k", "v") if kind != "i8" else ("k_scale", "v_scale")
+    bad = {"bf16": 0xff, "e4m3": 0x7f, "i8": 255}[kind]
     for r in range(2):
-        for i in range(int(host[2][r + 1] - host[2][r])):
+        n, full = int(host[2][r + 1] - host[2][r]), int(host[1][r]) // page
+        for i in range(n):
             row = int(host[2][r]) + i
             for h in range(heads):
-                keep = [t.clone() for t in tensors if t is not None]
-                used = set(int(b) for b in blocks[row, h])
-                full = int(host[1][r]) // page
-                for b in range(full):
-                    if b not in used:
-                        for t in (cache.k, cache.v):
-                            t.view(torch.uint8)[int(host[0][r, b])] = 0xff if kind == "bf16" else 0x7f
-                for j in range(int(host[2][r + 1] - host[2][r])):
-                    if not (int(mask[row, 0]) >> j) & 1:
-                        p = int(host[1][r]) + j
-                        for t in (cache.k, cache.v):
-                            t.view(torch.uint8)[int(host[0][r, p // page]), :, p % page] = 0xff if kind == "bf16" else 0x7f
-                got = D.dflash_sparse_attention(q, cache, gpu(blocks), **kw)
-                assert torch.equal(got[row, 4 * h:4 * h + 4], out[row, 4 * h:4 * h + 4])
-                for t, was in zip([t for t in tensors if t is not None], keep):
-                    t.view(torch.uint8).copy_(was.view(torch.uint8))
+                keep = [getattr(cache, name).clone() for name in names]
+                used = {int(b) for b in blocks[row, h]}
+                for name in names:
+                    t = getattr(cache, name).view(torch.uint8)
+                    t[host[0][r, [b for b in range(full) if b not in used]].tolist()] = bad
+                    for j in range(n):
+                        if not (int(mask[row, 0]) >> j) & 1:
+                            p = int(host[1][r]) + j
+                            t[int(host[0][r, p // page]), :, p % page] = bad
+                got = codes_f64(D.dflash_sparse_attention(q, cache, gpu(blocks), **kw))
+                at = np.s_[row, 4 * h:4 * h + 4]
+                assert (np.abs(got[at] - want[at]) <= bound[at]).all(), (row, h)
+                # rows that see what is broken are NaN
+                others = [x for x in range(int(host[2][r]), int(host[2][r + 1]))
+                          if {int(b) for b in blocks[x, h] if b >= 0} - used or int(mask[x, 0]) & ~int(mask[row, 0]) & ((1 << n) - 1)]
+                for x in others:
+                    assert np.isnan(got[x, 4 * h:4 * h + 4]).any(), (row, x, h)
+                for name, was in zip(names, keep):
+                    getattr(cache, name).view(torch.uint8).copy_(was.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("start", [40, 700])
+def test_infinities_that_one_node_sees(kind, start):
+    require_gpu()
+    say(f"infinity {kind} {start}")
+    page, heads, dim = 8, 1, 64
+    cache, tensors, plan, host, n_rows = written(kind, [start], [3], page, heads, dim)
+    full = start // page                                 # 87 blocks: keys for two workgroups
+    blocks = np.full((n_rows, heads, full), -1, dtype=np.int32)
+    blocks[0, 0], blocks[1, 0, :full - 1] = range(full), [b for b in range(full) if b != 1]
+    p = int(host[0][0, 1])
+    if kind == "bf16":
+        cache.v[p, 0, 3, 5], cache.v[p, 0, 4, 6] = float("inf"), -float("inf")
+    else:
+        cache.v.view(torch.uint8)[p, 0, 3, 5] = 0x7f
+    q, out, kw = check_sparse(cache, tensors, plan, host, n_rows, 3, np.where(blocks == 1, -1, blocks))
+    got = D.dflash_sparse_attention(q, cache, gpu(blocks), **kw).float()
+    assert not torch.isfinite(got[0, :, 5]).any() and torch.isfinite(got[0, :, 7:]).all() and torch.isfinite(got[1:3]).all()
+    if kind == "bf16":
+        assert (got[0, :, 5] == float("inf")).all() and (got[0, :, 6] == -float("inf")).all()
 
 
 def test_pages_outside_the_pool_and_lengths_beyond_the_table():
