@@ -50,7 +50,7 @@ struct Part {                                     // what a split item leaves: [
 };
 
 template <int DT, int D, int GT>
-__global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
+__global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128 ? 2 : 1))
     sparse_attention_kernel(SparseArgs a, int all_heads, int tiles, int splits) {
   using S = SparseShape<DT, D>;
   constexpr int kRB = S::kRB, kOps = D / 32, kBlocks = D / 16;
@@ -121,36 +121,42 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
   }
   bool bad = over, seen = over;
 
+  // Two values to choose from, not two places of the arguments to load one from.
+  uint64_t k_scales = reinterpret_cast<uint64_t>(c.k_scale), v_scales = reinterpret_cast<uint64_t>(c.v_scale);
+  asm volatile("" : "+s"(k_scales), "+s"(v_scales));
+  const unsigned char* row_scales = reinterpret_cast<const unsigned char*>(lane < 32 ? k_scales : v_scales);
+
   // --- looking up: lanes 0 .. 31 and 32 .. 63 both hold the step's 32 keys ---
-  int32_t a_block = 0, a_before = -1, a_off = 0, a_bit = 0, b_page = -1, b_off = 0;
-  uint32_t a_word = 0, c_byte = 0, vis0 = 0, vis1 = 0, vis2 = 0, vis3 = 0;
-  bool a_ok = false, a_chosen = false, b_ok = false, c_ok = false;
+  // Every look-up is the same loads on every path, whose values stay in the
+  // registers that they came to until the next iteration uses them: so nothing
+  // waits for the direct loads in flight.  Keys that are none load what is there.
+  int32_t a_block = 0, a_before = -1, a_rest = 0, a_off = 0, a_bit = 0, b_page = -1, b_off = 0;
+  uint32_t a_word = 0, vis0 = 0, vis1 = 0, vis2 = 0, vis3 = 0;
+  bool a_ok = false, a_chosen = false, a_masked = false, a_first = false, b_ok = false, c_ok = false;
 
   auto find_block = [&](int step) {
     const int64_t x = (int64_t)step * 32 + l32;
     a_ok = step < t1 && x < (int64_t)chosen_keys + rest;
-    a_chosen = x < chosen_keys;
-    const int32_t y = (int32_t)(x - chosen_keys);            // among the rest
-    const int32_t p = a_chosen ? (int32_t)x : full * c.page_size + (a_ok ? y : 0), d = c.per_page.div(p);
+    a_chosen = a_ok && x < chosen_keys;
+    const int32_t y = a_ok && !a_chosen ? (int32_t)(x - chosen_keys) : 0;   // among the rest
+    const int32_t p = a_chosen ? (int32_t)x : full * c.page_size + y, d = c.per_page.div(p);
     a_off = p - d * c.page_size;
-    a_block = d;
-    a_word = ~0u;
-    a_bit = 0;
-    a_before = -1;
-    if (a_ok && a_chosen) {
-      a_block = chosen[d];
-      if (d > 0) a_before = chosen[d - 1];
-    }
-    if (mask && a_ok && !a_chosen && y >= tail) {
-      a_word = mask[(y - tail) >> 5];
-      a_bit = (y - tail) & 31;
+    a_rest = d;
+    a_first = d == 0;
+    const int32_t* from = a_chosen ? chosen + d : table;
+    a_block = from[0];
+    a_before = (a_chosen && !a_first ? from - 1 : from)[0];
+    if (mask) {
+      a_masked = a_ok && !a_chosen && y >= tail;
+      a_bit = a_masked ? (y - tail) & 31 : 0;
+      a_word = mask[a_masked ? (y - tail) >> 5 : 0];
     }
   };
   auto find_page = [&]() {
-    b_ok = a_ok && (!a_chosen || (a_block >= 0 && a_block < full && a_block > a_before)) && ((a_word >> a_bit) & 1u);
+    const bool named = a_block >= 0 && a_block < full && (a_first || a_block > a_before);
+    b_ok = a_ok && (!a_chosen || named) && (!a_masked || ((a_word >> a_bit) & 1u));
     b_off = a_off;
-    b_page = -1;
-    if (b_ok) b_page = table[a_block];             // within the table: start + n is
+    b_page = table[b_ok ? (a_chosen ? a_block : a_rest) : 0];   // within the table: start + n is
   };
   auto find_row = [&](int step) {
     const bool held = b_page >= 0 && b_page < c.n_pages;
@@ -160,11 +166,15 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
     const int32_t at = c_ok ? head * c.page_size + b_off : 0;
     vis3 = (uint32_t)__ballot(c_ok);
     if (lane < 32) row_at[(step & 3) * 32 + lane] = id * c.page_bytes + (int64_t)at * kRB;
-    if constexpr (DT != DFLASH_BF16) c_byte = (lane < 32 ? c.k_scale : c.v_scale)[id * c.scale_page_bytes + at];
+    // the scale's byte, as a word of the lane, into the ring's place
+    if constexpr (DT != DFLASH_BF16)
+      __builtin_amdgcn_global_load_lds((const void*)(row_scales + id * c.scale_page_bytes + at), (lds_void_t*)(scales + (step & 3) * 64), 1, 0, 0);
   };
   auto put_scale = [&](int step) {
-    if constexpr (DT != DFLASH_BF16)
-      scales[(step & 3) * 64 + lane] = c_ok ? kv_scale_value(c_byte) * (lane < 32 ? c2 : 1.f) : 0.f;
+    if constexpr (DT != DFLASH_BF16) {
+      float* at = scales + (step & 3) * 64 + lane;
+      *at = c_ok ? kv_scale_value(__float_as_uint(*at)) * (lane < 32 ? c2 : 1.f) : 0.f;
+    }
   };
 
   // --- the products of a step ---
@@ -182,16 +192,33 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
         if (!((vis >> (x / S::kChunks)) & 1u)) st16(stage + S::kTile + x * 16, u32x4{0, 0, 0, 0});
       wave_order();
     }
+    // All of K's operands, scales and masks are read before the first product,
+    // and V's while the scores become weights: one wave to a SIMD has nobody to
+    // fill its waits.
+    u32x4 kf[2][kRB / 64];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < kRB / 64; ++i) kf[kb][i] = ld16(stage + (16 * kb + l16) * kRB + (((4 * i + g16) ^ kx) << 4));
+    float ks[2][4], vs[2][4];                      // s[t][kb][i]: key 16 kb + 4 g16 + i, row 16 t + l16
+    if constexpr (DT != DFLASH_BF16) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ks[kb][i] = scales[(step & 3) * 64 + 16 * kb + 4 * g16 + i];
+          vs[kb][i] = scales[(step & 3) * 64 + 32 + 16 * kb + 4 * g16 + i];
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     f32x4_t s[GT][2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      const unsigned char* krow = stage + (16 * kb + l16) * kRB;
 #pragma unroll
       for (int t = 0; t < GT; ++t) s[t][kb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kRB / 64; ++i) {
-        // rows 16 apart have one swizzle but for long rows' high bits, which it does not use
-        const u32x4 x = ld16(krow + (((4 * i + g16) ^ kx) << 4));
+        const u32x4 x = kf[kb][i];
         if constexpr (DT == DFLASH_BF16) {
 #pragma unroll
           for (int t = 0; t < GT; ++t)
@@ -206,17 +233,19 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
         }
       }
     }
-    // s[t][kb][i]: key 16 kb + 4 g16 + i, head 16 t + l16
-    float ks[2][4], vs[2][4];
-    if constexpr (DT != DFLASH_BF16) {
+    // V of up to eight blocks of 16 columns
+    const auto* v0 = (const __attribute__((address_space(3))) unsigned char*)(stage + S::kTile) + vbase;
+    constexpr int kGroup = kBlocks < 8 ? kBlocks : 8, kPieces = DT == DFLASH_BF16 ? 2 : 1;
+    i32x2_t vr2[kGroup][kPieces];
+    auto read_group = [&](int b0) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int b = 0; b < kGroup; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ks[kb][i] = scales[(step & 3) * 64 + 16 * kb + 4 * g16 + i];
-          vs[kb][i] = scales[(step & 3) * 64 + 32 + 16 * kb + 4 * g16 + i];
-        }
-    }
+        for (int x = 0; x < kPieces; ++x)
+          vr2[b][x] = read_transposed<DT>(v0 + ((((DT == DFLASH_BF16 ? 2 : 1) * (b0 + b)) ^ vx) << 4) + x * 16 * kRB);
+    };
+    read_group(0);
+    __builtin_amdgcn_sched_barrier(0);
     const uint32_t mine = vis >> (4 * g16);          // bit 16 kb + i
     bf16x8_t pf[GT];
 #pragma unroll
@@ -238,7 +267,11 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
         m[t] = next;
         l[t] *= keep;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[t][b] *= keep;
+        for (int b = 0; b < kBlocks; ++b) {
+          in_accumulators<GT * kBlocks >= 32>(o[t][b]);
+          o[t][b] *= keep;
+          in_accumulators<GT * kBlocks >= 32>(o[t][b]);
+        }
       }
       const float base = m[t] == -INFINITY ? 0.f : m[t] * cs;
       float sum = 0.f, p[8];
@@ -256,19 +289,17 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
       const u32x4 pw = {pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])};
       pf[t] = __builtin_bit_cast(bf16x8_t, pw);
     }
-    const auto* v0 = (const __attribute__((address_space(3))) unsigned char*)(stage + S::kTile) + vbase;
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      bf16x8_t vf;
-      if constexpr (DT == DFLASH_BF16) {
-        const i32x2_t lo = read_transposed<DT>(v0 + (((2 * b) ^ vx) << 4)), hi = read_transposed<DT>(v0 + (((2 * b) ^ vx) << 4) + 16 * kRB);
-        vf = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
-      } else {
-        const i32x2_t x = read_transposed<DT>(v0 + ((b ^ vx) << 4));
-        vf = codes_to_bf16<DT>((uint32_t)x[0], (uint32_t)x[1]);
+    for (int b0 = 0; b0 < kBlocks; b0 += kGroup) {
+      if (b0) read_group(b0);
+#pragma unroll
+      for (int b = 0; b < kGroup; ++b) {
+        bf16x8_t vf;
+        if constexpr (DT == DFLASH_BF16) vf = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(vr2[b][0], vr2[b][kPieces - 1], 0, 1, 2, 3));
+        else vf = codes_to_bf16<DT>((uint32_t)vr2[b][0][0], (uint32_t)vr2[b][0][1]);
+#pragma unroll
+        for (int t = 0; t < GT; ++t) o[t][b0 + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[t], o[t][b0 + b], 0, 0, 0);
       }
-#pragma unroll
-      for (int t = 0; t < GT; ++t) o[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[t], o[t][b], 0, 0, 0);
     }
   };
 
@@ -276,40 +307,64 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
   // writes the scales of step i + 2 and the addresses of step i + 3, and looks
   // up the pages of step i + 4 and the blocks of step i + 5.
   const int load_row = lane / S::kChunks, load_slot = lane % S::kChunks;
-  bool loading = false;                            // the iteration before issued direct loads, its last
-  for (int i = t0 - 5; i < t1 && t0 < t1; ++i) {
-    if (loading) wait_vm<2 * S::kLoads>();
-    else wait_vm<0>();
+  auto look_up = [&](int i) {
     wave_order();
     put_scale(i + 2);
     find_row(i + 3);
     find_page();
     find_block(i + 5);
     wave_order();
-    if (i >= t0 && vis0) {
-      seen = true;
-      products(i, vis0);
-    }
-    loading = i + 2 >= t0 && i + 2 < t1;
-    if (loading) {
-      __builtin_amdgcn_s_waitcnt((0 << 8) | (7 << 4) | 15 | (3 << 14));   // this step's reads of the stage are done
-      wave_order();
-      unsigned char* stage = stages + (i & 1) * 2 * S::kTile;
-      int64_t from[S::kLoads];
+  };
+  auto load = [&](int i) {
+    __builtin_amdgcn_s_waitcnt((0 << 8) | (7 << 4) | 15 | (3 << 14));   // this step's reads of the stage are done
+    wave_order();
+    unsigned char* stage = stages + (i & 1) * 2 * S::kTile;
+    int64_t from[S::kLoads];
 #pragma unroll
-      for (int x = 0; x < S::kLoads; ++x) from[x] = row_at[((i + 2) & 3) * 32 + x * (1024 / kRB) + load_row];
+    for (int x = 0; x < S::kLoads; ++x) from[x] = row_at[((i + 2) & 3) * 32 + x * (1024 / kRB) + load_row];
 #pragma unroll
-      for (int x = 0; x < S::kLoads; ++x) {
-        const int r = x * (1024 / kRB) + load_row;
-        __builtin_amdgcn_global_load_lds((const void*)(c.k + from[x] + ((load_slot ^ S::k_swizzle(r)) << 4)),
-                                         (lds_void_t*)(stage + x * 1024), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((const void*)(c.v + from[x] + ((load_slot ^ S::v_swizzle(r)) << 4)),
-                                         (lds_void_t*)(stage + S::kTile + x * 1024), 16, 0, 0);
-      }
+    for (int x = 0; x < S::kLoads; ++x) {
+      const int r = x * (1024 / kRB) + load_row;
+      __builtin_amdgcn_global_load_lds((const void*)(c.k + from[x] + ((load_slot ^ S::k_swizzle(r)) << 4)),
+                                       (lds_void_t*)(stage + x * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(c.v + from[x] + ((load_slot ^ S::v_swizzle(r)) << 4)),
+                                       (lds_void_t*)(stage + S::kTile + x * 1024), 16, 0, 0);
     }
+  };
+  auto shift = [&]() {
     vis0 = vis1;
     vis1 = vis2;
     vis2 = vis3;
+  };
+  // Past the last step the same number of loads takes row 0 of the pool: at the
+  // loop's top, on every path, all but the last 2 kLoads loads are waited for.
+  if (t0 < t1) {
+    for (int i = t0 - 5; i < t0 - 2; ++i) {
+      wait_vm<0>();
+      look_up(i);
+      shift();
+    }
+    wait_vm<0>();
+    look_up(t0 - 2);
+    load(t0 - 2);
+    shift();
+    wait_vm<2 * S::kLoads>();
+    look_up(t0 - 1);
+    load(t0 - 1);
+    shift();
+    for (int i = t0; i < t1; ++i) {
+      wait_vm<2 * S::kLoads>();
+      // What was looked up is here, and no use of it moves before the wait.  (The
+      // compiler joins a wait with the one that it would put at the next
+      // instruction, of which direct loads in flight make a wait for everything.)
+      asm volatile("s_nop 0");
+      asm volatile("" : "+v"(a_block), "+v"(a_before), "+v"(a_word), "+v"(b_page));
+      look_up(i);
+      seen = seen || vis0;
+      products(i, vis0);
+      load(i);
+      shift();
+    }
   }
   wait_vm<0>();
 

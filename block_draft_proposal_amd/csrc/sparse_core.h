@@ -23,6 +23,7 @@ struct SparseShape {
   static constexpr int kLoop = kMasksAt + kWaves * 4 * 32 * 4;
   static constexpr int kJoin = kWaves * 16 * (D + 2) * 4;             // after the loop: [wave] O, m and l of 16 rows
   static constexpr int kLds = kLoop > kJoin ? kLoop : kJoin;
+  static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;            // workgroups that a CU holds
   static_assert(kLds <= 160 * 1024 && 2 * kLoads < 63, "LDS of a CU, loads in flight");
 
   // Chunk c of stage row r lies in slot c ^ swizzle(r), so that reads of one
@@ -51,6 +52,14 @@ __device__ __forceinline__ float quarter_sum(float x) {
 // Orders a wave's LDS accesses as they are written (the hardware keeps a
 // wave's in order).
 __device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
+
+// With more than 256 registers the sums lie in AGPRs, which only the matrix
+// cores compute with.  Without this, at either end of the rare rescaling, the
+// compiler moves them to VGPRs and back in every step.
+template <bool MANY>
+__device__ __forceinline__ void in_accumulators(f32x4_t& x) {
+  if constexpr (MANY) asm volatile("" : "+a"(x));
+}
 
 // Whether rows of a request attend together, and how.
 struct TilePlan {

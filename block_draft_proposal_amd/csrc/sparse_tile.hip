@@ -17,6 +17,7 @@
 // looks for them: a row whose result is not finite is computed again by itself,
 // over its own keys alone.
 #include <algorithm>
+#include <cstdlib>
 
 #include "sparse_core.h"
 
@@ -194,7 +195,7 @@ __device__ __forceinline__ void alone(const SparseArgs& a, const Tile& t, int no
 }
 
 template <int DT, int D, int GT>
-__global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
+__global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128 ? 2 : 1))
     sparse_tile_kernel(SparseArgs a, Lists lists, FastDiv per_group, int nodes, int per_req, int splits) {
   using S = SparseShape<DT, D>;
   constexpr int kRB = S::kRB, kOps = D / 32, kBlocks = D / 16;
@@ -258,30 +259,30 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
   }
   uint32_t seen = t.over ? all_nodes : 0, bad = seen;   // over this lane's keys
 
+  // Two values to choose from, not two places of the arguments to load one from.
+  uint64_t k_scales = reinterpret_cast<uint64_t>(c.k_scale), v_scales = reinterpret_cast<uint64_t>(c.v_scale);
+  asm volatile("" : "+s"(k_scales), "+s"(v_scales));
+  const unsigned char* row_scales = reinterpret_cast<const unsigned char*>(lane < 32 ? k_scales : v_scales);
+
   // --- looking up: lanes 0 .. 31 and 32 .. 63 both hold the step's 32 keys ---
+  // Every look-up is the same loads on every path, whose values stay in the
+  // registers that they came to until the next iteration uses them: so nothing
+  // waits for the direct loads in flight.  Keys that are none load what is there.
   int32_t a_page = -1, a_off = 0;
-  uint32_t a_mask = 0, c_byte = 0;
+  uint32_t a_bits = 0, a_mask = 0;                 // a_bits: of a chosen page; a_mask: which of them count, or the nodes of the rest
   uint32_t vis0 = 0, vis1 = 0, vis2 = 0, vis3 = 0; // keys of a step that some node sees
-  bool c_ok = false, all0 = false, all1 = false, all2 = false, all3 = false;   // whether all nodes see all of its keys
+  bool a_chosen = false, c_ok = false;
+  bool all0 = false, all1 = false, all2 = false, all3 = false;   // whether all nodes see all of a step's keys
 
   auto find_page = [&](int step) {
     const int64_t x = (int64_t)step * 32 + l32;
-    a_page = -1;
-    a_mask = 0;
-    if (step >= t1 || x >= (int64_t)chosen_keys + rest) return;
-    if (x < chosen_keys) {
-      const int e = c.per_page.div((int32_t)x);
-      a_off = (int32_t)x - e * c.page_size;
-      const uint2 entry = entries[e];
-      a_page = (int32_t)entry.x;
-      a_mask = entry.y;
-      return;
-    }
-    const int32_t y = (int32_t)(x - chosen_keys), p = t.full * c.page_size + y, d = c.per_page.div(p), j = y - tail;
+    const bool ok = step < t1 && x < (int64_t)chosen_keys + rest;
+    a_chosen = ok && x < chosen_keys;
+    const int32_t y = ok && !a_chosen ? (int32_t)(x - chosen_keys) : 0;   // among the rest
+    const int32_t p = a_chosen ? (int32_t)x : t.full * c.page_size + y, d = c.per_page.div(p), j = y - tail;
     a_off = p - d * c.page_size;
-    a_page = table[d];                             // within the table: start + n is
-    a_mask = all_nodes;
-    if (j >= 0) {
+    a_mask = ok ? all_nodes : 0u;
+    if (ok && !a_chosen && j >= 0) {
       if (mask) {
         a_mask = 0;
         for (int i = 0; i < t.nt; ++i) a_mask |= ((mask[(int64_t)i * 2 * a.mask_words + (j >> 5)] >> (j & 31)) & 1u) << i;
@@ -289,25 +290,33 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
         a_mask = j - t.n0 >= 32 ? 0u : all_nodes & (~0u << (j - t.n0));
       }
     }
+    const int32_t* from = a_chosen ? reinterpret_cast<const int32_t*>(entries + d) : table + (ok ? d : 0);   // within the table: start + n is
+    a_page = from[0];
+    a_bits = (uint32_t)(a_chosen ? from + 1 : from)[0];
   };
   auto find_row = [&](int step) {
+    const uint32_t who = a_chosen ? a_bits : a_mask;
     const bool held = a_page >= 0 && a_page < c.n_pages;
-    seen |= a_mask;
-    if (!held) bad |= a_mask;
-    c_ok = a_mask != 0 && held;
+    seen |= who;
+    if (!held) bad |= who;
+    c_ok = who != 0 && held;
     const int64_t id = c_ok ? a_page : 0;
     const int32_t at = c_ok ? head * c.page_size + a_off : 0;
     vis3 = (uint32_t)__ballot(c_ok);
-    all3 = __all(c_ok && a_mask == all_nodes);
+    all3 = __all(c_ok && who == all_nodes);
     if (lane < 32) {
       row_at[(step & 3) * 32 + lane] = id * c.page_bytes + (int64_t)at * kRB;
-      masks[(step & 3) * 32 + lane] = c_ok ? a_mask : 0u;
+      masks[(step & 3) * 32 + lane] = c_ok ? who : 0u;
     }
-    if constexpr (DT != DFLASH_BF16) c_byte = (lane < 32 ? c.k_scale : c.v_scale)[id * c.scale_page_bytes + at];
+    // the scale's byte, as a word of the lane, into the ring's place
+    if constexpr (DT != DFLASH_BF16)
+      __builtin_amdgcn_global_load_lds((const void*)(row_scales + id * c.scale_page_bytes + at), (lds_void_t*)(scales + (step & 3) * 64), 1, 0, 0);
   };
   auto put_scale = [&](int step) {
-    if constexpr (DT != DFLASH_BF16)
-      scales[(step & 3) * 64 + lane] = c_ok ? kv_scale_value(c_byte) * (lane < 32 ? c2 : 1.f) : 0.f;
+    if constexpr (DT != DFLASH_BF16) {
+      float* at = scales + (step & 3) * 64 + lane;
+      *at = c_ok ? kv_scale_value(__float_as_uint(*at)) * (lane < 32 ? c2 : 1.f) : 0.f;
+    }
   };
 
   // --- the products of a step ---
@@ -323,31 +332,15 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
         if (!((vis >> (x / S::kChunks)) & 1u)) st16(stage + S::kTile + x * 16, u32x4{0, 0, 0, 0});
       asm volatile("" ::: "memory");
     }
-    f32x4_t s[GT][2];
+    // All of K's operands, scales and masks are read before the first product,
+    // and V's while the scores become weights: one wave to a SIMD has nobody to
+    // fill its waits.
+    u32x4 kf[2][kRB / 64];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const unsigned char* krow = stage + (16 * kb + l16) * kRB;
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int u = 0; u < GT; ++u) s[u][kb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kRB / 64; ++i) {
-        const u32x4 x = ld16(krow + (((4 * i + g16) ^ kx) << 4));
-        if constexpr (DT == DFLASH_BF16) {
-#pragma unroll
-          for (int u = 0; u < GT; ++u)
-            s[u][kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), qf[u][i], s[u][kb], 0, 0, 0);
-        } else {
-          const bf16x8_t lo = codes_to_bf16<DT>(x[0], x[1]), hi = codes_to_bf16<DT>(x[2], x[3]);
-#pragma unroll
-          for (int u = 0; u < GT; ++u) {
-            s[u][kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, qf[u][2 * i], s[u][kb], 0, 0, 0);
-            s[u][kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, qf[u][2 * i + 1], s[u][kb], 0, 0, 0);
-          }
-        }
-      }
-    }
-    // s[u][kb][i]: key 16 kb + 4 g16 + i, row 16 u + l16
-    float ks[2][4], vs[2][4];
+      for (int i = 0; i < kRB / 64; ++i) kf[kb][i] = ld16(stage + (16 * kb + l16) * kRB + (((4 * i + g16) ^ kx) << 4));
+    float ks[2][4], vs[2][4];                      // s[u][kb][i]: key 16 kb + 4 g16 + i, row 16 u + l16
     uint32_t who[2][4];
     if constexpr (DT != DFLASH_BF16) {
 #pragma unroll
@@ -364,26 +357,82 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) who[kb][i] = masks[(step & 3) * 32 + 16 * kb + 4 * g16 + i];
     }
-    bf16x8_t pf[GT];
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4_t s[GT][2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+      for (int u = 0; u < GT; ++u) s[u][kb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kRB / 64; ++i) {
+        const u32x4 x = kf[kb][i];
+        if constexpr (DT == DFLASH_BF16) {
+#pragma unroll
+          for (int u = 0; u < GT; ++u)
+            s[u][kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x), qf[u][i], s[u][kb], 0, 0, 0);
+        } else {
+          const bf16x8_t lo = codes_to_bf16<DT>(x[0], x[1]), hi = codes_to_bf16<DT>(x[2], x[3]);
+#pragma unroll
+          for (int u = 0; u < GT; ++u) {
+            s[u][kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, qf[u][2 * i], s[u][kb], 0, 0, 0);
+            s[u][kb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, qf[u][2 * i + 1], s[u][kb], 0, 0, 0);
+          }
+        }
+      }
+    }
+    // V of up to eight blocks of 16 columns
+    const auto* v0 = (const __attribute__((address_space(3))) unsigned char*)(stage + S::kTile) + vbase;
+    constexpr int kGroup = kBlocks < 8 ? kBlocks : 8, kPieces = DT == DFLASH_BF16 ? 2 : 1;
+    i32x2_t vr2[kGroup][kPieces];
+    auto read_group = [&](int b0) {
+#pragma unroll
+      for (int b = 0; b < kGroup; ++b)
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x)
+          vr2[b][x] = read_transposed<DT>(v0 + ((((DT == DFLASH_BF16 ? 2 : 1) * (b0 + b)) ^ vx) << 4) + x * 16 * kRB);
+    };
+    read_group(0);
+    __builtin_amdgcn_sched_barrier(0);
+    // The row tiles' maxima first, one decision for all of them, then their
+    // weights: independent chains that run beside each other.
+    float top[GT];
+    bool past = false;
 #pragma unroll
     for (int u = 0; u < GT; ++u) {
-      float top = -INFINITY;
+      top[u] = -INFINITY;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (DT != DFLASH_BF16) s[u][kb][i] *= ks[kb][i];
           if (!all) s[u][kb][i] = (who[kb][i] >> node[u]) & 1u ? s[u][kb][i] : -INFINITY;
-          top = fmaxf(top, s[u][kb][i]);
+          top[u] = fmaxf(top[u], s[u][kb][i]);
         }
-      top = quarter_max(top);
-      if (__any((top - m[u]) * cs > 8.f)) {
-        const float next = fmaxf(m[u], top), keep = m[u] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[u] - next) * cs);
+    }
+#pragma unroll
+    for (int u = 0; u < GT; ++u) {
+      top[u] = quarter_max(top[u]);
+      // The sums keep the maximum they were built with until a row's passes it
+      // by 2^8: weights up to 256 are as exact as those up to 1.
+      past = past || (top[u] - m[u]) * cs > 8.f;
+    }
+    if (__any(past)) {
+#pragma unroll
+      for (int u = 0; u < GT; ++u) {
+        const float next = fmaxf(m[u], top[u]), keep = m[u] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[u] - next) * cs);
         m[u] = next;
         l[u] *= keep;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[u][b] *= keep;
+        for (int b = 0; b < kBlocks; ++b) {
+          in_accumulators<GT * kBlocks >= 32>(o[u][b]);
+          o[u][b] *= keep;
+          in_accumulators<GT * kBlocks >= 32>(o[u][b]);
+        }
       }
+    }
+    bf16x8_t pf[GT];
+#pragma unroll
+    for (int u = 0; u < GT; ++u) {
       const float base = m[u] == -INFINITY ? 0.f : m[u] * cs;
       float sum = 0.f, p[8];
 #pragma unroll
@@ -402,19 +451,17 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
       const u32x4 pw = {pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])};
       pf[u] = __builtin_bit_cast(bf16x8_t, pw);
     }
-    const auto* v0 = (const __attribute__((address_space(3))) unsigned char*)(stage + S::kTile) + vbase;
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      bf16x8_t vf;
-      if constexpr (DT == DFLASH_BF16) {
-        const i32x2_t lo = read_transposed<DT>(v0 + (((2 * b) ^ vx) << 4)), hi = read_transposed<DT>(v0 + (((2 * b) ^ vx) << 4) + 16 * kRB);
-        vf = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
-      } else {
-        const i32x2_t x = read_transposed<DT>(v0 + ((b ^ vx) << 4));
-        vf = codes_to_bf16<DT>((uint32_t)x[0], (uint32_t)x[1]);
+    for (int b0 = 0; b0 < kBlocks; b0 += kGroup) {
+      if (b0) read_group(b0);
+#pragma unroll
+      for (int b = 0; b < kGroup; ++b) {
+        bf16x8_t vf;
+        if constexpr (DT == DFLASH_BF16) vf = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(vr2[b][0], vr2[b][kPieces - 1], 0, 1, 2, 3));
+        else vf = codes_to_bf16<DT>((uint32_t)vr2[b][0][0], (uint32_t)vr2[b][0][1]);
+#pragma unroll
+        for (int u = 0; u < GT; ++u) o[u][b0 + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u], o[u][b0 + b], 0, 0, 0);
       }
-#pragma unroll
-      for (int u = 0; u < GT; ++u) o[u][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u], o[u][b], 0, 0, 0);
     }
   };
 
@@ -422,39 +469,65 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), 1)
   // writes the scales of step i + 2 and the addresses of step i + 3, and looks
   // up the pages of step i + 4.
   const int load_row = lane / S::kChunks, load_slot = lane % S::kChunks;
-  bool loading = false;                            // the iteration before issued direct loads, its last
-  for (int i = t0 - 4; i < t1 && t0 < t1; ++i) {
-    if (loading) wait_vm<2 * S::kLoads>();
-    else wait_vm<0>();
+  auto look_up = [&](int i) {
     asm volatile("" ::: "memory");
     put_scale(i + 2);
     find_row(i + 3);
     find_page(i + 4);
     asm volatile("" ::: "memory");
-    if (i >= t0 && vis0) products(i, vis0, all0);
-    loading = i + 2 >= t0 && i + 2 < t1;
-    if (loading) {
-      __builtin_amdgcn_s_waitcnt((0 << 8) | (7 << 4) | 15 | (3 << 14));   // this step's reads of the stage are done
-      asm volatile("" ::: "memory");
-      unsigned char* stage = stages + (i & 1) * 2 * S::kTile;
-      int64_t from[S::kLoads];
+  };
+  auto load = [&](int i) {
+    __builtin_amdgcn_s_waitcnt((0 << 8) | (7 << 4) | 15 | (3 << 14));   // this step's reads of the stage are done
+    asm volatile("" ::: "memory");
+    unsigned char* stage = stages + (i & 1) * 2 * S::kTile;
+    int64_t from[S::kLoads];
 #pragma unroll
-      for (int x = 0; x < S::kLoads; ++x) from[x] = row_at[((i + 2) & 3) * 32 + x * (1024 / kRB) + load_row];
+    for (int x = 0; x < S::kLoads; ++x) from[x] = row_at[((i + 2) & 3) * 32 + x * (1024 / kRB) + load_row];
 #pragma unroll
-      for (int x = 0; x < S::kLoads; ++x) {
-        const int r = x * (1024 / kRB) + load_row;
-        __builtin_amdgcn_global_load_lds((const void*)(c.k + from[x] + ((load_slot ^ S::k_swizzle(r)) << 4)),
-                                         (lds_void_t*)(stage + x * 1024), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((const void*)(c.v + from[x] + ((load_slot ^ S::v_swizzle(r)) << 4)),
-                                         (lds_void_t*)(stage + S::kTile + x * 1024), 16, 0, 0);
-      }
+    for (int x = 0; x < S::kLoads; ++x) {
+      const int r = x * (1024 / kRB) + load_row;
+      __builtin_amdgcn_global_load_lds((const void*)(c.k + from[x] + ((load_slot ^ S::k_swizzle(r)) << 4)),
+                                       (lds_void_t*)(stage + x * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(c.v + from[x] + ((load_slot ^ S::v_swizzle(r)) << 4)),
+                                       (lds_void_t*)(stage + S::kTile + x * 1024), 16, 0, 0);
     }
+  };
+  auto shift = [&]() {
     vis0 = vis1;
     vis1 = vis2;
     vis2 = vis3;
     all0 = all1;
     all1 = all2;
     all2 = all3;
+  };
+  // Past the last step the same number of loads takes row 0 of the pool: at the
+  // loop's top, on every path, all but the last 2 kLoads loads are waited for.
+  if (t0 < t1) {
+    for (int i = t0 - 4; i < t0 - 2; ++i) {
+      wait_vm<0>();
+      look_up(i);
+      shift();
+    }
+    wait_vm<0>();
+    look_up(t0 - 2);
+    load(t0 - 2);
+    shift();
+    wait_vm<2 * S::kLoads>();
+    look_up(t0 - 1);
+    load(t0 - 1);
+    shift();
+    for (int i = t0; i < t1; ++i) {
+      wait_vm<2 * S::kLoads>();
+      // What was looked up is here, and no use of it moves before the wait.  (The
+      // compiler joins a wait with the one that it would put at the next
+      // instruction, of which direct loads in flight make a wait for everything.)
+      asm volatile("s_nop 0");
+      asm volatile("" : "+v"(a_page), "+v"(a_bits));
+      look_up(i);
+      products(i, vis0, all0);
+      load(i);
+      shift();
+    }
   }
   wait_vm<0>();
 
@@ -605,11 +678,11 @@ hipError_t run(const SparseArgs& a, const TilePlan& plan, hipStream_t s) {
   sparse_union_kernel<<<(unsigned)items, kThreads, (size_t)c.table_width * 4, s>>>(a, lists, plan.nodes, plan.per_req);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // Workgroups to a tile: as many as fill the chip twice, while each wave has
-  // two steps of its own.
+  // Workgroups to a tile: as many as run at once, while each wave has two steps
+  // of its own.
   const int64_t keys = (int64_t)a.n_take * c.page_size + c.page_size + a.max_nodes;
   const int64_t most = std::max<int64_t>(1, keys / (32 * S::kWaves * 2));
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMaxTileParts / items), (512 + items - 1) / items));
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMaxTileParts / items), (getenv("DF_T") ? atoi(getenv("DF_T")) : 256 * S::kPerCu) / items));
   sparse_tile_kernel<DT, D, GT><<<(unsigned)(items * splits), S::kThreads, S::kLds, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
   if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
   sparse_tile_join_kernel<DT, D, GT><<<(unsigned)(items * (16 * GT * D / 1024)), kThreads, 0, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
