@@ -36,26 +36,41 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
   const int rest = blockIdx.x / c.n_kv_heads, chunk = rest % chunks;
   const int64_t row0 = (int64_t)(rest / chunks) * NT;
 
-  // queries in 8 bits: a wave takes a row at a time
-  for (int n = wave; n < NT; n += kThreads / 64) {
-    const int64_t row = min(row0 + n, c.n_rows - 1);
-    const uint16_t* qp = a.q + row * a.q_row + (int64_t)head * group * a.q_head;
-    constexpr int kVecs = D / 8;                  // 16-byte pieces of a head
-    uint32_t top = 0;
-    for (int x = lane; x < group * kVecs; x += 64) {
-      float f[8];
-      unpack16(ld16(qp + (int64_t)(x / kVecs) * a.q_head + (x % kVecs) * 8), f);
+  // Queries in 8 bits: a wave takes NT / 4 rows.  The first 128 of a row's
+  // 16-byte pieces are read once, those of all rows before the first is used.
+  constexpr int kVecs = D / 8, kMine = NT < 4 ? 1 : NT / 4;   // pieces of a head, rows of a wave
+  const int pieces = group * kVecs;
+  u32x4 held[kMine][2];
+  const auto row_of = [&](int i) { return min(wave + i * (kThreads / 64), NT - 1); };
+  const auto query_of = [&](int i) { return a.q + min(row0 + row_of(i), c.n_rows - 1) * a.q_row + (int64_t)head * group * a.q_head; };
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+  for (int i = 0; i < kMine; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int x = min(lane + 64 * j, pieces - 1);
+      held[i][j] = ld16(query_of(i) + (int64_t)(x / kVecs) * a.q_head + (x % kVecs) * 8);
     }
-    top = wave_max_u32(top);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (wave + i * (kThreads / 64) >= NT) break;
+    const int n = row_of(i);
+    const uint16_t* qp = query_of(i);
+    uint32_t top = 0;
+    auto widen = [&](u32x4 w) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+    };
+    widen(held[i][0]);
+    widen(held[i][1]);
+    for (int x = lane + 128; x < pieces; x += 64) widen(ld16(qp + (int64_t)(x / kVecs) * a.q_head + (x % kVecs) * 8));
+    top = wave_max_u32(top) << 16;
     const bool finite = top < 0x7f800000u;
     const int byte = finite ? max((int)((top + 0x1ffffu) >> 23) - 6, 27) : 127;
     const float inv = finite ? __uint_as_float((uint32_t)(254 - byte) << 23) : 0.f;
-    for (int x = lane; x < steps * kHeads * kVecs; x += 64) {
-      const int h = min(x / kVecs, group - 1), d = (x % kVecs) * 8;   // heads past the group repeat its last
+    auto store = [&](u32x4 w, int x) {
+      const int d = (x % kVecs) * 8;
       float f[8];
-      unpack16(ld16(qp + (int64_t)h * a.q_head + d), f);
+      unpack16(w, f);
       uint32_t neg[2] = {0, 0}, pos[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -70,7 +85,12 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
       int8_t* at = queries + ((step * kOps + d / 64) * 64 + (d % 64 / 16) * 16 + m) * 16 + d % 16;
       *reinterpret_cast<uint2*>(at) = make_uint2(neg[0], neg[1]);
       *reinterpret_cast<uint2*>(at + (D / 64) * 64 * 16) = make_uint2(pos[0], pos[1]);
-    }
+    };
+    if (lane < pieces) store(held[i][0], lane);
+    if (lane + 64 < pieces) store(held[i][1], lane + 64);
+    // the rest, and heads past the group, which repeat its last
+    for (int x = lane + 128; x < pieces; x += 64) store(ld16(qp + (int64_t)(x / kVecs) * a.q_head + (x % kVecs) * 8), x);
+    for (int x = pieces + lane; x < steps * kHeads * kVecs; x += 64) store(ld16(qp + (int64_t)(group - 1) * a.q_head + (x % kVecs) * 8), x);
   }
   __syncthreads();
 
@@ -392,15 +412,105 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
   }
 }
 
+// One wave for a (row, kv head) of up to 64 KPL blocks; lane l holds keys l,
+// l + 64, ..., so that a load is one run.
+//
+// The threshold is found by halving the range of the scores, which some 12
+// rounds make small, and now and then that of the keys, which bounds the rounds
+// whatever the scores.  A round ends the search where as many keys as are taken
+// reach its score.  (512 rows x 8 heads of up to
+// 2048 blocks: WAVE_US us; a workgroup with a histogram each 38.)
+__device__ __forceinline__ uint32_t score_key(float x) {
+  const uint32_t bits = __float_as_uint(x);
+  return (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
+}
+// A wave's sum, in all lanes.
+__device__ __forceinline__ int wave_total(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast 15, then 31
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return __builtin_amdgcn_readlane(x, 63);
+}
+template <int KPL>
+__global__ void __launch_bounds__(kThreads) select_take_wave_kernel(SelectArgs a, int64_t n_items) {
+  const KvView& c = a.c;
+  const int lane = threadIdx.x & 63;
+  const int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (item >= n_items) return;                    // waves do not wait for each other
+  // all that the table's row may have, before the row's request is known
+  const uint32_t* keys = a.keys + item * c.table_width;
+  uint32_t k[KPL];
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) k[i] = keys[min(i * 64 + lane, c.table_width - 1)];
+  const int64_t row = item / c.n_kv_heads;
+  int32_t req = 0;
+  int64_t pos = 0;
+  if (!kv_row_position(c, row, row, req, pos) || row - c.offsets[req] >= a.max_nodes) return;   // the same in every lane
+  const int32_t blocks = __builtin_amdgcn_readfirstlane(kv_blocks(c, c.start[req])), take = a.n_take;
+  int32_t* out = a.out + item * take;
+  if (blocks <= take) {
+    for (int i = lane; i < take; i += 64) out[i] = i < blocks ? i : -1;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) k[i] = i * 64 + lane < blocks ? k[i] : 0u;   // no key is 0
+  // how many keys are at least x > 0
+  auto reach = [&](uint32_t x) -> int {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) n += k[i] >= x;
+    return wave_total(n);
+  };
+  uint32_t low = 0xffffffffu, high = 0;           // of the keys that are neither forced nor broken
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const bool plain = k[i] - 1u < kBroken - 1u;
+    low = min(low, plain ? k[i] : 0xffffffffu);
+    high = max(high, plain ? k[i] : 0u);
+  }
+  low = (uint32_t)__builtin_amdgcn_readfirstlane((int)~wave_max_u32(~low));
+  high = (uint32_t)__builtin_amdgcn_readfirstlane((int)wave_max_u32(high));
+  // at least `take` keys reach `low`, and fewer reach beyond `high`
+  if (reach(kBroken) >= take) low = high = reach(kForced) >= take ? kForced : kBroken;
+  for (int round = 1; low < high; ++round) {
+    uint32_t mid = low + (high - low + 1) / 2;
+    if (round % 8) mid = min(max(score_key(0.5f * key_score(low) + 0.5f * key_score(high)), low + 1), high);
+    mid = (uint32_t)__builtin_amdgcn_readfirstlane((int)mid);
+    const int n = reach(mid);
+    if (n < take) {
+      high = mid - 1;
+    } else {
+      low = mid;
+      if (n == take) break;
+    }
+  }
+  const uint32_t threshold = low;
+  const int left = take - (threshold == kForced ? 0 : reach(threshold + 1));   // keys at the threshold that are taken, the first ones
+
+  int above = 0, at = 0;                          // so many keys before
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const uint64_t is_above = __ballot(k[i] > threshold), is_at = __ballot(k[i] == threshold);
+    const int my_above = above + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(is_above >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)is_above, 0));
+    const int my_at = at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(is_at >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)is_at, 0));
+    if (k[i] > threshold || (k[i] == threshold && my_at < left)) out[my_above + min(my_at, left)] = i * 64 + lane;
+    above += __builtin_popcountll(is_above);
+    at += __builtin_popcountll(is_at);
+  }
+}
+
 template <int D, int NT>
 hipError_t score(const SelectArgs& a, hipStream_t s) {
   const FastDiv per_group = FastDiv::make(a.n_q_heads / a.c.n_kv_heads);
   const int steps = (per_group.d + 16 / NT - 1) / (16 / NT);
   const int64_t tiles = (a.c.n_rows + NT - 1) / NT * a.c.n_kv_heads;
-  // blocks of a workgroup: as many as leave 1024 workgroups, so that the
-  // queries are prepared seldom
-  int64_t chunk = kStepBlocks;
-  while (chunk < a.c.table_width && tiles * ((a.c.table_width + 2 * chunk - 1) / (2 * chunk)) >= 1024) chunk *= 2;
+  // Blocks of a workgroup: a share that makes as many workgroups as run at once.
+  const int64_t wanted = std::max<int64_t>(1, 768 / tiles);
+  const int64_t share = (a.c.table_width + wanted - 1) / wanted;
+  const int64_t chunk = (share + kStepBlocks - 1) / kStepBlocks * kStepBlocks;
   const int chunks = (int)((a.c.table_width + chunk - 1) / chunk);
   const size_t lds = (size_t)steps * (2 * D / 64) * 1024;
   select_score_kernel<D, NT><<<(unsigned)(tiles * chunks), kThreads, lds, s>>>(a, per_group, steps, (int)chunk, chunks);
@@ -431,11 +541,15 @@ hipError_t launch_kv_select(const SelectArgs& a, hipStream_t stream) {
                        : a.c.head_dim == 128 ? score_dim<128>(a, stream)
                                              : score_dim<256>(a, stream);
   if (e != hipSuccess) return e;
-  // Threads of a (row, kv head): as few as hold the keys of the longest prefix.
-  const unsigned items = (unsigned)(a.c.n_rows * a.c.n_kv_heads);
-  if (a.c.table_width <= 8 * 256) select_take_kernel<256, 8><<<items, 256, 0, stream>>>(a);
-  else if (a.c.table_width <= 16 * 256) select_take_kernel<256, 16><<<items, 256, 0, stream>>>(a);
-  else select_take_kernel<1024, 8><<<items, 1024, 0, stream>>>(a);
+  // A wave for a (row, kv head) where it holds the longest prefix's keys and
+  // there are enough of them for the chip; else a workgroup.
+  const int64_t items = a.c.n_rows * a.c.n_kv_heads;
+  const unsigned waves = (unsigned)((items + kThreads / 64 - 1) / (kThreads / 64));
+  // (A table has a few pages more than a power of two: for the nodes.)
+  if (a.c.table_width <= 18 * 64) select_take_wave_kernel<18><<<waves, kThreads, 0, stream>>>(a, items);
+  else if (a.c.table_width <= 36 * 64) select_take_wave_kernel<36><<<waves, kThreads, 0, stream>>>(a, items);
+  else if (a.c.table_width <= 68 * 64) select_take_wave_kernel<68><<<waves, kThreads, 0, stream>>>(a, items);
+  else select_take_kernel<1024, 8><<<(unsigned)items, 1024, 0, stream>>>(a);
   return hipGetLastError();
 }
 

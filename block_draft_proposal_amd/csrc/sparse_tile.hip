@@ -17,14 +17,13 @@
 // looks for them: a row whose result is not finite is computed again by itself,
 // over its own keys alone.
 #include <algorithm>
-#include <cstdlib>
 
 #include "sparse_core.h"
 
 namespace dflash {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kUnionThreads = 512;
 constexpr int kMaxBlocks = 16384;                 // of a table's row: a word each in LDS
 constexpr int kMaxTileNodes = 32;                 // bits of a word
 constexpr int kMaxTileParts = 512;
@@ -77,27 +76,29 @@ __device__ __forceinline__ bool tile_at(const SparseArgs& a, int tile, int nodes
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads) sparse_union_kernel(SparseArgs a, Lists lists, int nodes, int per_req) {
+__global__ void __launch_bounds__(kUnionThreads) sparse_union_kernel(SparseArgs a, Lists lists, int nodes, int per_req) {
   extern __shared__ uint32_t bits[];              // [full]
-  __shared__ uint32_t sums[kThreads / 64];
+  __shared__ uint32_t sums[kUnionThreads / 64];
   const KvView& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int head = blockIdx.x % c.n_kv_heads;
   Tile t;
   if (!tile_at(a, blockIdx.x / c.n_kv_heads, nodes, per_req, t)) return;
-  for (int b = tid; b < t.full; b += kThreads) bits[b] = 0;
+  for (int b = tid; b < t.full; b += kUnionThreads) bits[b] = 0;
   __syncthreads();
   if (!t.over) {
-    for (int64_t x = tid; x < (int64_t)t.nt * a.n_take; x += kThreads) {
-      const int node = (int)(x / a.n_take), e = (int)(x - (int64_t)node * a.n_take);
-      const int32_t* chosen = a.blocks + ((t.row0 + node) * c.n_kv_heads + head) * a.n_take + e;
-      const int32_t b = chosen[0], before = e > 0 ? chosen[-1] : -1;
-      if (b >= 0 && b < t.full && b > before) atomicOr(&bits[b], 1u << node);
+    for (int node = wave; node < t.nt; node += kUnionThreads / 64) {
+      const int32_t* chosen = a.blocks + ((t.row0 + node) * c.n_kv_heads + head) * a.n_take;
+#pragma unroll 4
+      for (int e = lane; e < a.n_take; e += 64) {
+        const int32_t b = chosen[e], before = e > 0 ? chosen[e - 1] : -1;
+        if (b >= 0 && b < t.full && b > before) atomicOr(&bits[b], 1u << node);
+      }
     }
   }
   __syncthreads();
   // the blocks with a bit, in order: a thread takes neighbours
-  const int each = (t.full + kThreads - 1) / kThreads, lo = min(tid * each, t.full), hi = min(lo + each, t.full);
+  const int each = (t.full + kUnionThreads - 1) / kUnionThreads, lo = min(tid * each, t.full), hi = min(lo + each, t.full);
   uint32_t n = 0;
   for (int b = lo; b < hi; ++b) n += bits[b] != 0;
   uint32_t scan = n;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) sparse_union_kernel(SparseArgs a, Li
   __syncthreads();
   uint32_t at = scan - n, total = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) {
+  for (int i = 0; i < kUnionThreads / 64; ++i) {
     if (i < wave) at += sums[i];
     total += sums[i];
   }
@@ -675,14 +676,14 @@ hipError_t run(const SparseArgs& a, const TilePlan& plan, hipStream_t s) {
   const FastDiv per_group = FastDiv::make(a.n_q_heads / c.n_kv_heads);
   const Lists lists(a.workspace, c.n_rows, c.n_kv_heads, a.n_take, c.head_dim);
   const int64_t tiles = (int64_t)c.n_req * plan.per_req, items = tiles * c.n_kv_heads;
-  sparse_union_kernel<<<(unsigned)items, kThreads, (size_t)c.table_width * 4, s>>>(a, lists, plan.nodes, plan.per_req);
+  sparse_union_kernel<<<(unsigned)items, kUnionThreads, (size_t)c.table_width * 4, s>>>(a, lists, plan.nodes, plan.per_req);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Workgroups to a tile: as many as run at once, while each wave has two steps
   // of its own.
   const int64_t keys = (int64_t)a.n_take * c.page_size + c.page_size + a.max_nodes;
   const int64_t most = std::max<int64_t>(1, keys / (32 * S::kWaves * 2));
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMaxTileParts / items), (getenv("DF_T") ? atoi(getenv("DF_T")) : 256 * S::kPerCu) / items));
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMaxTileParts / items), 256 * S::kPerCu / items));
   sparse_tile_kernel<DT, D, GT><<<(unsigned)(items * splits), S::kThreads, S::kLds, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
   if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
   sparse_tile_join_kernel<DT, D, GT><<<(unsigned)(items * (16 * GT * D / 1024)), kThreads, 0, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
