@@ -241,6 +241,10 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
   __shared__ uint32_t found[3], n_few, range[2];
   const KvView& c = a.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // what the table's row may have, before the row's request is known
+  const uint32_t* keys = a.keys + (int64_t)blockIdx.x * c.table_width;
+  uint32_t k[kOwn];
+  load_keys<T, kOwn>(keys, tid, 0, c.table_width, k);
   const int64_t row = blockIdx.x / (unsigned)c.n_kv_heads;
   int32_t req = 0;
   int64_t pos = 0;
@@ -251,10 +255,9 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
     for (int i = tid; i < take; i += T) out[i] = i < blocks ? i : -1;
     return;
   }
-  const uint32_t* keys = a.keys + (int64_t)blockIdx.x * c.table_width;
   const bool held = blocks <= kSegment;           // the keys stay in registers
-  uint32_t k[kOwn];
-  load_keys<T, kOwn>(keys, tid, 0, blocks, k);
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) k[i] = tid * kOwn + i < blocks ? k[i] : 0u;   // no key is 0
   int at_sum = 0;
   // calls f for every key (and for the zeros past the last)
   auto for_keys = [&](auto f) {

@@ -101,9 +101,12 @@ class KVBounds:
 
 
 def _rows(pool: KVPool, page_table: torch.Tensor, lens: torch.Tensor) -> RowsStruct:
-    _kv._i32(page_table, "page_table", 2, pool.device)
-    _vector(lens, "lens", page_table.shape[0], pool.device)
-    n_req, width = _kv._int32(page_table.shape[0], "page_table's rows"), _kv._int32(page_table.shape[1], "page_table's width")
+    device = pool.device
+    _kv._i32(page_table, "page_table", 2, device)
+    n_req, width = page_table.shape
+    _vector(lens, "lens", n_req, device)
+    if n_req > 0x7FFFFFFF or width > 0x7FFFFFFF:
+        raise ValueError("page_table's shape does not fit 32 bits")
     return RowsStruct(page_table.data_ptr(), page_table.stride(0) if n_req > 1 else width, width, n_req, lens.data_ptr())
 
 
@@ -128,9 +131,10 @@ def _workspace(pool: KVPool, rows: RowsStruct, workspace, stream):
 
 
 def _lists(pool: KVPool, copies, counts, n: int, stream):
-    with _kv._on(stream):
-        copies = torch.empty((n, 2), dtype=torch.int32, device=pool.device) if copies is None else copies
-        counts = torch.empty(2, dtype=torch.int32, device=pool.device) if counts is None else counts
+    if copies is None or counts is None:
+        with _kv._on(stream):
+            copies = torch.empty((n, 2), dtype=torch.int32, device=pool.device) if copies is None else copies
+            counts = torch.empty(2, dtype=torch.int32, device=pool.device) if counts is None else counts
     _pairs(copies, pool.device)
     _vector(counts, "counts", 2, pool.device)
     return copies, counts

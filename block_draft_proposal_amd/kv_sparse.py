@@ -89,7 +89,8 @@ def dflash_kv_select(q: torch.Tensor, bounds: "_pages.KVBounds", *, page_table: 
     if out.dtype != torch.int32 or out.dim() != 3 or out.shape[:2] != (n_rows, bounds.n_kv_heads) or not out.is_contiguous() or \
             out.device != bounds.device or n_take not in (None, out.shape[2]):
         raise ValueError("out must be contiguous int32 [n_rows, n_kv_heads, n_take] on the bounds' GPU")
-    workspace = _space(_fns().dflash_kv_select_workspace_size(bounds.ref, n_rows, batch.table_width), workspace, bounds.device, stream)
+    workspace = _space(0 if workspace is not None else
+                       _fns().dflash_kv_select_workspace_size(bounds.ref, n_rows, batch.table_width), workspace, bounds.device, stream)
     _kv._call(_fns().dflash_kv_select, bounds, stream, bounds.ref, ctypes.byref(batch), q.data_ptr(), *_kv._strides(q),
               _kv._int32(n_q_heads, "n_q_heads"), _kv._int32(max_nodes, "max_nodes"), _kv._int32(out.shape[2], "n_take"),
               _kv._int32(n_first, "n_first"), _kv._int32(n_last, "n_last"), _b._dtype_code(q), out.data_ptr(),
