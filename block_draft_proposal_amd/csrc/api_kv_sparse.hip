@@ -10,8 +10,10 @@ namespace {
 using namespace dflash;
 
 constexpr int kMaxGroup = 64, kMaxNodes = 4096, kMaxTake = 65536;
-// Workgroups of 256 threads, and rows times kv heads, in one launch.
-constexpr int64_t kMaxGroups = kMaxThreads / 256;
+// Rows times kv heads of a call: up to 1024 threads each, in one launch.
+constexpr int64_t kMaxItems = (int64_t)1 << 21;
+// Requests whose pages' bounds one call makes: a workgroup each.
+constexpr int32_t kMaxRequests = 1 << 20;
 // Blocks of a request that keys are kept of.
 constexpr int32_t kMaxBlocks = 1 << 24;
 
@@ -61,6 +63,7 @@ int dflash_kv_bounds(const dflash_kv_cache* cache, const dflash_page_bounds* bou
   if (meets_cache(c, bounds->codes, code_size) || meets_cache(c, bounds->scale, scale_size))
     return fail(DFLASH_ERR_INVALID_ARG, "%s: the bounds overlap the cache", who);
   if (c.n_req == 0) return ok();
+  if (c.n_req > kMaxRequests) return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_req > 2^20", who);
   if (!end) return fail(DFLASH_ERR_INVALID_ARG, "%s: null end", who);
   const size_t n = (size_t)c.n_req * 4, table = ((size_t)(c.n_req - 1) * c.table_stride + c.table_width) * 4;
   const struct { const void* p; size_t bytes; } arrays[] = {{c.table, table}, {c.start, n}, {end, n}};
@@ -75,7 +78,7 @@ size_t dflash_kv_select_workspace_size(const dflash_page_bounds* bounds, int64_t
   size_t code_size = 0, scale_size = 0;
   if (check_bounds(bounds, code_size, scale_size, "dflash_kv_select_workspace_size") != DFLASH_OK) return 0;
   ok();
-  if (n_rows <= 0 || n_rows > kMaxGroups / bounds->n_kv_heads || table_width < 1 || table_width > kMaxBlocks) return 0;
+  if (n_rows <= 0 || n_rows > kMaxItems / bounds->n_kv_heads || table_width < 1 || table_width > kMaxBlocks) return 0;
   return kv_select_bytes(n_rows, bounds->n_kv_heads, table_width);
 }
 
@@ -97,8 +100,8 @@ int dflash_kv_select(const dflash_page_bounds* bounds, const dflash_kv_batch* ba
   if (n_first < 0 || n_last < 0 || (int64_t)n_first + n_last > n_take)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: need n_first, n_last >= 0 and n_first + n_last <= n_take", who);
   if (a.c.n_req == 0 || a.c.n_rows == 0) return ok();
-  if (a.c.n_rows > kMaxGroups / bounds->n_kv_heads)
-    return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_rows * n_kv_heads must be below 2^24", who);
+  if (a.c.n_rows > kMaxItems / bounds->n_kv_heads)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_rows * n_kv_heads must be at most 2^21", who);
   if (a.c.table_width > kMaxBlocks) return fail(DFLASH_ERR_UNSUPPORTED, "%s: table_width > 2^24", who);
   size_t qb = 0;
   if ((st = check_rows(q, q_row_stride, q_head_stride, a.c.n_rows, n_q_heads, bounds->head_dim, 2, qb, "q", who)) != DFLASH_OK)
@@ -139,7 +142,7 @@ size_t dflash_sparse_attention_workspace_size(const dflash_kv_cache* cache, int6
   KvView c;
   if (view_cache(cache, c, "dflash_sparse_attention_workspace_size") != DFLASH_OK) return 0;
   ok();
-  if (n_rows <= 0 || n_rows > kMaxGroups / c.n_kv_heads || n_take < 0 || n_take > kMaxTake || n_q_heads < 1 ||
+  if (n_rows <= 0 || n_rows > kMaxItems / c.n_kv_heads || n_take < 0 || n_take > kMaxTake || n_q_heads < 1 ||
       n_q_heads % c.n_kv_heads || n_q_heads / c.n_kv_heads > kMaxGroup || max_nodes < 1 || max_nodes > kMaxNodes)
     return 0;
   return sparse_attention_bytes(c, n_rows, n_take, max_nodes, n_q_heads);
@@ -164,8 +167,8 @@ int dflash_sparse_attention(const dflash_kv_cache* cache, const dflash_kv_batch*
   if ((int64_t)n_take * a.c.page_size > (1 << 30))
     return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_take * page_size must be at most 2^30", who);
   if (a.c.n_req == 0 || a.c.n_rows == 0) return ok();   // a mask of no rows may be null
-  if (a.c.n_rows > kMaxGroups / a.c.n_kv_heads)
-    return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_rows * n_kv_heads must be below 2^24", who);
+  if (a.c.n_rows > kMaxItems / a.c.n_kv_heads)
+    return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_rows * n_kv_heads must be at most 2^21", who);
   if (mask ? mask_words < (max_nodes + 63) / 64 : mask_words != 0)
     return fail(DFLASH_ERR_INVALID_ARG, "%s: mask_words must be >= ceil(max_nodes / 64) with a mask, 0 without", who);
   if (reinterpret_cast<uintptr_t>(mask) & 7) return fail(DFLASH_ERR_INVALID_ARG, "%s: mask must be 8-byte aligned", who);

@@ -152,8 +152,8 @@ __device__ __forceinline__ Change change_of(const PagesView& v, const int32_t* w
 // A page's count changes by `by` for every request of a group that lets it go or
 // takes it.  Requests that share a prefix follow one another and hold the same
 // page in the same column: a thread adds up what neighbours do to one page (512
-// samples of 64 prompts, pages of 16 and 8 to a page: let go 3.0 us and forked
-// 6.3, an atomic for each entry 7.7 and 12.9).
+// samples of 64 prompts, pages of 16 and 8 to a page: let go 5.0 us and forked
+// 7.6, an atomic for each entry 7.7 and 12.9).
 struct Tally {
   int32_t page = -1, by = 0;
   __device__ __forceinline__ void flush(const PagesView& v) {
@@ -296,7 +296,7 @@ __device__ __forceinline__ int grant_of(const Grant* grants, int lo, int hi, int
 // Each free page of a rank below plan.pages goes to the request whose share it
 // lies in.  A chunk's pages have neighbouring ranks: its requests are looked up
 // once, and their shares lie in LDS (512 requests, a pool of half a million
-// pages: ASSIGN_US; a search in memory for each page 22 us).  Workgroups behind
+// pages: 7 us; a search in memory for each page 22 us).  Workgroups behind
 // the chunks set the lengths.
 constexpr int kShares = 2048;
 __global__ void __launch_bounds__(kThreads) resize_assign_kernel(PagesView v, const int32_t* want, Space s, int chunks, int32_t* copies) {
@@ -734,7 +734,7 @@ int parts_of(const PagesView& v, int each) {
 }
 unsigned groups_of(const PagesView& v) { return (unsigned)((v.n_req + kGroup - 1) / kGroup); }
 // One launch where one workgroup is enough: beams of 4 x 8 requests, resize
-// SMALL_RESIZE us and the steps apart MANY_RESIZE.
+// 5.6 us and the steps apart 15.0.
 bool small_tables(const PagesView& v) {
   return v.n_req <= kSmallRequests && (int64_t)v.n_req * v.table_width <= kSmallEntries;
 }

@@ -168,9 +168,10 @@ __global__ void __launch_bounds__(kThreads) select_score_kernel(SelectArgs a, Fa
         }
         if constexpr (NT == 1) best[t][0] = max(best[t][0], best[t][1]);
         const int64_t b = b0 + 16 * t + (lane & 15);
-        // whole numbers below 2^23 times a power of two: exact, and normal
-        // numbers for any scale byte from 27 on once 2^-20 is taken off
-        const float unit = kv_scale_value(byte[t] == 255u ? 127u : (uint32_t)max((int)byte[t] - 20, 0));
+        // whole numbers up to 2^22 times a power of two: exact.  With 2^-24
+        // taken off, for any scale byte from 25 on, they are 0 or normal numbers
+        // and so is a difference of two of them.
+        const float unit = kv_scale_value(byte[t] == 255u ? 127u : (uint32_t)max((int)byte[t] - 24, 1));
         constexpr int kRegs = NT < 4 ? NT : 4;
         const int groups = NT < 4 ? 1 : NT / 4;   // lane groups that hold rows of their own
 #pragma unroll
@@ -231,7 +232,7 @@ __device__ __forceinline__ float key_score(uint32_t key) { return __uint_as_floa
 // few keys share it they are ranked one by one; else the bin is the next range.
 // Bins are even in the score, not in the key's bits: scores of one magnitude
 // share their upper bits, and all threads adding to one bin would wait in line
-// (one row of 8192 blocks: 11 bits of the key at a time 29 us, so TAKE_1).
+// (one row of 8192 blocks, 8 heads: 11 bits of the key at a time 29 us, so 10).
 template <int T, int kOwn>
 __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
   constexpr int kSegment = kOwn * T, kBins = 8 * T < 2048 ? 8 * T : 2048, kEach = kBins / T, kFew = 64;
@@ -303,9 +304,11 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
 #pragma unroll 1
     while (low < high) {
       // the least key is in the first bin and the greatest in the last, and a
-      // greater score never in a lower bin
+      // greater score never in a lower bin; so every round leaves a smaller range
       const float least = key_score(low), span = key_score(high) - least;
-      auto bin_of = [&](uint32_t key) { return (int)((key_score(key) - least) / span * (float)(kBins - 1)); };
+      auto bin_of = [&](uint32_t key) {
+        return key == high ? kBins - 1 : min((int)((key_score(key) - least) / span * (float)(kBins - 1)), kBins - 1);
+      };
       for_keys([&](uint32_t key) {
         if (key >= low && key <= high) atomicAdd(&bins[bin_of(key)], 1u);
       });
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
 // rounds make small, and now and then that of the keys, which bounds the rounds
 // whatever the scores.  A round ends the search where as many keys as are taken
 // reach its score.  (512 rows x 8 heads of up to
-// 2048 blocks: WAVE_US us; a workgroup with a histogram each 38.)
+// 2048 blocks: 27 us; a workgroup with a histogram each 38.)
 __device__ __forceinline__ uint32_t score_key(float x) {
   const uint32_t bits = __float_as_uint(x);
   return (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;

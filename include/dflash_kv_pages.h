@@ -19,7 +19,9 @@
  * Results do not depend on the order in which anything runs.
  *
  * A page p is free where refs[p] is 0, held by refs[p] requests where it is
- * above, and never given or moved where it is below.  Request r holds the
+ * above, and never given or moved where it is below.  The counts are the
+ * caller's to begin with (zeros, and empty rows) and have to fit the tables; a
+ * call keeps them so.  Request r holds the
  * first ceil(lens[r] / page_size) entries of its row of page_table.  What lies
  * behind them is not read (resize, fork: entries that a call adds are written,
  * those that it takes off become -1).  Entries outside [0, n_pages) hold

@@ -42,6 +42,7 @@ extern "C" {
  *                nothing done for them.
  *   bounds       of the cache's pages and heads; may not overlap the cache or
  *                the batch's arrays
+ *   n_req        at most 2^20
  * Pages that two requests share may be given by both: they write the same. */
 int dflash_kv_bounds(const dflash_kv_cache* cache, const dflash_page_bounds* bounds, const dflash_kv_batch* batch,
                      const int32_t* end, dflash_stream_t stream);
@@ -70,8 +71,10 @@ int dflash_kv_bounds(const dflash_kv_cache* cache, const dflash_page_bounds* bou
  *   n_take  1 .. 65536, n_first and n_last >= 0 with n_first + n_last <= n_take
  *   max_nodes  1 .. 4096: no request has more rows
  *   n_q_heads  a multiple of n_kv_heads, up to 64 query heads to a kv head
- * A request whose start is below 0 or beyond the table's positions has as many
- * blocks as the table holds, or none.
+ * A request whose start is below 0 has no blocks, one whose start is beyond the
+ * table's positions as many as the table holds.  Scale bytes below 25, which
+ * dflash_kv_bounds does not write, count as 25.
+ * n_rows * n_kv_heads is at most 2^21, table_width at most 2^24.
  * Scratch: dflash_kv_select_workspace_size() bytes, 256-byte aligned; it never
  * falls with n_rows or table_width; calls that may run at the same time need
  * one each. */
@@ -95,17 +98,19 @@ int dflash_kv_select(const dflash_page_bounds* bounds, const dflash_kv_batch* ba
  *   q, mask, out, max_nodes, scale   as for dflash_tree_attention
  * A row that sees nothing gets zeros.  What a row does not see has no effect on
  * it, whatever values the cache holds there, but for the last bits: the nodes of
- * a request are taken together.  Positions without a page in the pool make the rows that see them NaN;
- * so do lengths beyond the table.
+ * a request are taken together.  Positions without a page in the pool make the
+ * rows that see them NaN; so do lengths beyond the table.
  * Arithmetic: as for dflash_tree_attention; an infinity or a NaN among the
  * values that a row sees makes its result an infinity or a NaN.  A call's
  * result is the same every time; its sums are split by the whole batch, so a
  * request may differ in the last bits from one batch to another.
  *   max_nodes also decides whether the nodes of a request are taken together:
  *           give the batch's own largest number, 1 for plain decoding.
+ * n_rows * n_kv_heads is at most 2^21, n_take * page_size at most 2^30.
  * Scratch: dflash_sparse_attention_workspace_size() bytes, 256-byte aligned; it
- * never falls with n_rows, n_take, max_nodes or n_q_heads; it may not overlap anything else of the call, and calls that may
- * run at the same time need one each. */
+ * never falls with n_rows, n_take, max_nodes or n_q_heads; it may not overlap
+ * anything else of the call, and calls that may run at the same time need one
+ * each. */
 size_t dflash_sparse_attention_workspace_size(const dflash_kv_cache* cache, int64_t n_rows, int32_t n_take,
                                               int32_t max_nodes, int32_t n_q_heads);
 int dflash_sparse_attention(const dflash_kv_cache* cache, const dflash_kv_batch* batch, const void* q,

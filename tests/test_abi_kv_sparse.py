@@ -55,7 +55,7 @@ def test_library_exports_every_declared_entry_point():
 
 
 BAD_BATCH = [(dict(n_req=-1), -1), (dict(table_width=0), -1), (dict(table_stride=3), -1), (dict(page_table=None), -1), (dict(start=None), -1)]
-BAD_ROWS = [(dict(n_rows=-1), -1), (dict(n_rows=1 << 31), -1), (dict(offsets=None), -1), (dict(n_rows=(1 << 21) + 1), -2)]
+BAD_ROWS = [(dict(n_rows=-1), -1), (dict(n_rows=1 << 31), -1), (dict(offsets=None), -1), (dict(n_rows=(1 << 18) + 1), -2)]
 BAD_BOUNDS = [(dict(codes=None), -1), (dict(scale=None), -1), (dict(codes=(12 << 40) + 8), -1), (dict(n_pages=0), -1), (dict(n_pages=1 << 31), -1),
               (dict(page_size=0), -1), (dict(page_size=65537), -1), (dict(n_kv_heads=0), -1), (dict(head_dim=96), -2),
               (dict(scale=(12 << 40) + 100), -1)]
@@ -81,6 +81,7 @@ def test_bounds_refusals():
                dict(codes=3 << 40), dict(scale=4 << 40), dict(scale=1 << 40), dict(scale=8 << 40)):
         assert _bounds(bounds=kw) == -1, kw
     assert _bounds(end=None) == -1
+    assert _bounds(batch=dict(n_req=(1 << 20) + 1)) == -2
     assert _bounds(cache=SCALED, bounds=dict(codes=6 << 40)) == -1
 
 
@@ -97,7 +98,7 @@ def test_select_refusals():
     size = lambda rows, width: S._fns().dflash_kv_select_workspace_size(_structs()[2], rows, width)  # noqa: E731
     assert size(8, 4) > 0 and _select(n=size(8, 4) - 1) == -3
     assert size(8, 5) >= size(8, 4) and size(9, 4) >= size(8, 4)
-    assert size(0, 4) == 0 and size(8, 0) == 0 and size((1 << 21) + 1, 4) == 0 and size(8, (1 << 24) + 1) == 0
+    assert size(0, 4) == 0 and size(8, 0) == 0 and size((1 << 18) + 1, 4) == 0 and size(8, (1 << 24) + 1) == 0
 
 
 def test_sparse_refusals():
@@ -117,8 +118,8 @@ def test_sparse_refusals():
     assert size() > 0 and _sparse(n=size() - 1) == -3
     last = 0
     for kw in (dict(nodes=1), dict(), dict(nodes=4096), dict(rows=9, nodes=4096), dict(rows=9, take=4), dict(rows=1000, take=4),
-               dict(rows=1 << 20, take=4), dict(rows=1 << 20, take=65536), dict(rows=1 << 20, take=65536, hq=512)):
+               dict(rows=1 << 18, take=4), dict(rows=1 << 18, take=65536), dict(rows=1 << 18, take=65536, hq=512)):
         assert size(**kw) >= last, kw
         last = size(**kw)
     assert size(take=0) > 0
-    assert size(rows=0) == size(hq=12) == size(hq=8 * 65) == size(take=-1) == size(nodes=0) == size(nodes=4097) == size(rows=1 << 22) == 0
+    assert size(rows=0) == size(hq=12) == size(hq=8 * 65) == size(take=-1) == size(nodes=0) == size(nodes=4097) == size(rows=(1 << 18) + 1) == 0

@@ -208,6 +208,26 @@ def test_select_broken_blocks_and_queries():
     check_select(q, b, (table, *plan[1:]), (host_table, *host[1:]), 40, n_first=20, n_last=20)
 
 
+@pytest.mark.parametrize("blocks", [900, 5000])
+def test_select_any_scale_byte(blocks):
+    """Scores over the whole range of the bytes, which no other kernel writes:
+    finite, and in order."""
+    require_gpu()
+    say(f"scale bytes {blocks}")
+    plan, host, n_pages, n_rows = make_plan([blocks, blocks - 7], [3, 2], 1, seed=6)
+    b = rand_bounds(n_pages, 2, 64, 1, 7)
+    b.scale.random_(25, 256)
+    b.scale[b.scale == 255] = 254                        # so that none is broken
+    b.codes[::3] = b.codes.amin(2, keepdim=True)[::3]    # scores of either sign
+    q = rand_rows(n_rows, 4, 64, "bf16", 8)
+    for take in (3, 400, blocks - 9):
+        check_select(q, b, plan, host, take, n_first=0, n_last=0)
+    b.scale.random_(0, 25)
+    low = D.KVBounds(b.codes, torch.full_like(b.scale, 25), page_size=1)
+    kw = dict(page_table=plan[0], start=plan[1], offsets=plan[2], max_nodes=3, n_take=400)
+    assert torch.equal(D.dflash_kv_select(q, b, **kw)[:host[2][-1]], D.dflash_kv_select(q, low, **kw)[:host[2][-1]])
+
+
 def test_select_leaves_the_rest_alone():
     """Rows beyond max_nodes and padding keep what they held; lengths out of range."""
     require_gpu()
