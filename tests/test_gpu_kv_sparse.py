@@ -228,6 +228,56 @@ def test_select_any_scale_byte(blocks):
     assert torch.equal(D.dflash_kv_select(q, b, **kw)[:host[2][-1]], D.dflash_kv_select(q, low, **kw)[:host[2][-1]])
 
 
+@pytest.mark.parametrize("dim,heads,group,page,nodes,n_req", [(64, 8, 2, 16, 16, 19), (128, 16, 5, 8, 8, 15), (256, 8, 3, 16, 12, 20), (128, 8, 4, 1, 6, 25)])
+def test_select_of_enough_rows_for_one_launch(dim, heads, group, page, nodes, n_req):
+    """Tiles that hold parts of several requests, requests without rows or without
+    blocks, and padding."""
+    require_gpu()
+    say(f"one launch {dim} {heads} {nodes}")
+    rng = np.random.default_rng(dim + nodes)
+    rows = rng.integers(0, nodes + 1, n_req)
+    rows[:3] = nodes, 0, nodes
+    start = rng.integers(0, 40 * page, n_req)
+    start[5:8] = 0, page - 1, 40 * page
+    plan, host, n_pages, n_rows = make_plan(start, rows, page, seed=3)
+    b = rand_bounds(n_pages, heads, dim, page, 5)
+    b.scale[::11] = 255
+    q = rand_rows(n_rows, heads * group, dim, "bf16", 6)
+    check_select(q, b, plan, host, 7, max_nodes=nodes)
+    check_select(q, b, plan, host, 12, n_first=3, n_last=2, max_nodes=nodes)
+    check_select(q, b, plan, host, 5, max_nodes=nodes - 1)
+
+
+@pytest.mark.parametrize("scores", ["spread", "few", "one", "wide"])
+@pytest.mark.parametrize("dim,nodes,n_req,blocks,take", [(128, 16, 18, 2000, 128), (64, 8, 33, 2300, 2200), (256, 16, 17, 700, 65), (64, 16, 40, 70, 64)])
+def test_a_batch_chooses_as_its_requests_alone(dim, nodes, n_req, blocks, take, scores):
+    """One launch for the batch's tiles, two for a request's few."""
+    require_gpu()
+    say(f"batch and alone {dim} {nodes} {blocks} {scores}")
+    rng = np.random.default_rng(blocks)
+    rows, start = np.full(n_req, nodes), rng.integers(blocks // 2, blocks + 1, n_req)
+    rows[1::3] = nodes // 2 + 1
+    start[0] = blocks
+    plan, host, n_pages, n_rows = make_plan(start, rows, 1, seed=4)
+    heads = 8
+    b = rand_bounds(n_pages, heads, dim, 1, 7, wide=1 if scores == "few" else 127, scales=1 if scores == "few" else 3)
+    if scores == "wide":
+        b.scale.random_(27, 250)
+    if scores == "one":
+        b.codes.fill_(3)
+        b.scale.fill_(127)
+    q = rand_rows(n_rows, heads, dim, "bf16", 8)
+    if scores == "few":
+        q = (q > 1).to(torch.bfloat16)
+    table, begin, offsets = plan
+    got = D.dflash_kv_select(q, b, page_table=table, start=begin, offsets=offsets, max_nodes=nodes, n_take=take)
+    for r in range(n_req):
+        lo, hi = int(host[2][r]), int(host[2][r + 1])
+        alone = D.dflash_kv_select(q[lo:hi], b, page_table=table[r:r + 1], start=begin[r:r + 1], offsets=gpu([0, hi - lo]),
+                                   max_nodes=nodes, n_take=take)
+        assert torch.equal(got[lo:hi], alone), r
+
+
 def test_select_leaves_the_rest_alone():
     """Rows beyond max_nodes and padding keep what they held; lengths out of range."""
     require_gpu()
