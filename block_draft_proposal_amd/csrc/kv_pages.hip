@@ -9,8 +9,8 @@
 // to all of the next.  Where one workgroup holds pool and tables, a call is one.
 //
 // Planning moves little and is bound by latency: its floor is the launches.
-// Measured: 512 requests in a pool of half a million pages, a resize 18 us (let go
-// 5.0, count 2.6, plan 4.1, give 7.1), a fork 10, a compact's planning 22 (128
+// Measured: 512 requests in a pool of half a million pages, a resize 17 us (let go
+// 5.0, count 2.6, plan 4.1, give 6.1), a fork 10, a compact's planning 22 (128
 // requests, 32768 pages); 32 requests in a small pool 4 to 6 us a call.  Copies of
 // pages stream: 0.53 GB, read and written in 190 us, 5.6 TB/s.
 #include <algorithm>
@@ -300,10 +300,10 @@ __device__ __forceinline__ int grant_of(const Grant* grants, int lo, int hi, int
 }
 
 // Each free page of a rank below plan.pages goes to the request whose share it
-// lies in.  A chunk's pages have neighbouring ranks: its requests are looked up
-// once, and their shares lie in LDS (512 requests, a pool of half a million
-// pages: 7 us; a search in memory for each page 22 us).  Workgroups behind
-// the chunks set the lengths.
+// lies in.  The shares lie in LDS: all of them, or those of the requests that a
+// chunk's pages go to, which have neighbouring ranks (512 requests, a pool of half
+// a million pages: 6 us; the chunk's requests searched for in memory 7, each page's
+// 22).  Workgroups behind the chunks set the lengths.
 constexpr int kShares = 2048;
 __global__ void __launch_bounds__(kThreads) resize_assign_kernel(PagesView v, const int32_t* want, Space s, int chunks, int32_t* copies) {
   __shared__ Grant shares[kShares];
@@ -320,24 +320,37 @@ __global__ void __launch_bounds__(kThreads) resize_assign_kernel(PagesView v, co
   if (first >= plan.pages) return;
   const int64_t base = (int64_t)blockIdx.x * kChunk + 4 * threadIdx.x;
   const Four f = load_four(v, base);
-  int32_t total, rank = first + chunk_ranks(f, IsFree(), total);
+  const bool all = v.n_req <= kShares;
+  if (all)
+    for (int i = threadIdx.x; i < v.n_req; i += kThreads) shares[i] = s.grants[i];
+  int32_t total, rank = first + chunk_ranks(f, IsFree(), total);   // behind its barriers the shares are there
   if (total == 0) return;
-  if (threadIdx.x < 2)
-    ends[threadIdx.x] = grant_of(s.grants, 0, v.n_req, threadIdx.x ? min(first + total, plan.pages) - 1 : first);
-  __syncthreads();
-  const int r0 = ends[0], n = ends[1] - r0 + 1;
-  const bool held = n <= kShares;
-  if (held) {
-    for (int i = threadIdx.x; i < n; i += kThreads) shares[i] = s.grants[r0 + i];
+  int r0 = 0, n = v.n_req;
+  if (!all) {
+    if (threadIdx.x < 2)
+      ends[threadIdx.x] = grant_of(s.grants, 0, v.n_req, threadIdx.x ? min(first + total, plan.pages) - 1 : first);
     __syncthreads();
+    r0 = ends[0];
+    n = ends[1] - r0 + 1;
+    if (n <= kShares) {
+      for (int i = threadIdx.x; i < n; i += kThreads) shares[i] = s.grants[r0 + i];
+      __syncthreads();
+    }
   }
+  const bool held = n <= kShares;
+  int r = -1;
+  int32_t next = 0;                               // where the share behind r's begins
+  Grant g;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (f.refs[i] != 0) continue;
     if (rank >= plan.pages) continue;
     const int32_t page = (int32_t)(base + i);
-    const int r = held ? r0 + grant_of(shares, 0, n, rank) : grant_of(s.grants, r0, r0 + n, rank);
-    const Grant g = held ? shares[r - r0] : s.grants[r];
+    if (r < 0 || rank >= next) {
+      r = held ? r0 + grant_of(shares, 0, n, rank) : grant_of(s.grants, r0, r0 + n, rank);
+      g = held ? shares[r - r0] : s.grants[r];
+      next = r + 1 >= r0 + n ? 0x7fffffff : held ? shares[r + 1 - r0].begin : s.grants[r + 1].begin;
+    }
     int32_t* row = v.table + r * v.table_stride;
     int32_t at = rank - g.begin;
     if (g.copy >= 0) {

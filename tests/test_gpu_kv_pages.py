@@ -374,3 +374,23 @@ def test_binding_refuses():
     with pytest.raises(D.DFlashError, match="bounds"):
         D.dflash_kv_copy_pages(cache, gpu([[0, 1]]), bounds=D.KVBounds.empty(other))
     b.check("nothing has changed")
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 5000])
+def test_pages_to_the_first_and_the_last_of_many_requests(n):
+    """Requests between them that take nothing, more than a workgroup keeps."""
+    require_gpu()
+    say(f"first and last of {n}")
+    page, width, n_pages = 4, 5, 20_000
+    refs, table, lens = gpu(np.zeros(n_pages)), gpu(np.full((n, width), -1)), gpu(np.zeros(n))
+    refs[::2] = -1
+    want = np.zeros(n)
+    want[0], want[1], want[n // 2], want[n - 1] = 9, 20, 1, 17
+    copies, counts = D.dflash_kv_resize(D.KVPool(refs, page), page_table=table, lens=lens, want=gpu(want))
+    assert counts.tolist() == [0, 0]
+    rows = table.cpu().numpy()
+    free = 1
+    for r, need in ((0, 3), (1, 5), (n // 2, 1), (n - 1, 5)):
+        assert rows[r].tolist() == [free + 2 * i for i in range(need)] + [-1] * (width - need), r
+        free += 2 * need
+    assert int((table >= 0).sum()) == 14 and int((refs == 1).sum()) == 14
