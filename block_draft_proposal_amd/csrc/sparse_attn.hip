@@ -26,8 +26,6 @@
 // heads, e4m3 (541 MB): 110 us, 4.9 TB/s, what a copy of 2 GB reaches on the same
 // card.  One row over 32 pages of 64, bf16 (8.4 MB): 10.8 us and 2.7 for the
 // join: look-ups, loads and products of a dozen steps one after the other.
-#include <algorithm>
-
 #include "sparse_core.h"
 
 namespace dflash {
@@ -61,7 +59,7 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   constexpr int kRB = S::kRB, kOps = D / 32, kBlocks = D / 16;
   extern __shared__ __align__(16) unsigned char sa_smem[];
   const KvView& c = a.c;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, g16 = lane >> 4, l32 = lane & 31;
   // rows of one kv head are neighbours on one XCD: a request's share pages
   const uint32_t w = xcd_contiguous(blockIdx.x, gridDim.x);
@@ -93,12 +91,12 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   used = over ? 0 : (int)wave_max_u32((uint32_t)used);
   const int32_t chosen_keys = used * c.page_size, tail = start - full * c.page_size;
   const int32_t rest = over ? 0 : tail + (a.mask ? n : node + 1);
-  const int64_t steps = ((int64_t)chosen_keys + rest + 31) / 32, slots = (int64_t)splits * S::kWaves, me = split * S::kWaves + wave;
+  const int64_t steps = ((int64_t)chosen_keys + rest + 31) / 32, slots = (int64_t)splits * waves, me = split * waves + wave;
   const int t0 = __builtin_amdgcn_readfirstlane((int)(steps * me / slots)), t1 = __builtin_amdgcn_readfirstlane((int)(steps * (me + 1) / slots));
 
-  unsigned char* stages = sa_smem + wave * S::kWaveStages;
-  int64_t* row_at = reinterpret_cast<int64_t*>(sa_smem + S::kRowsAt) + wave * 4 * 32;
-  float* scales = reinterpret_cast<float*>(sa_smem + S::kScalesAt) + wave * 4 * 64;
+  unsigned char* stages = sa_smem + wave * S::kWaveLds;
+  int64_t* row_at = reinterpret_cast<int64_t*>(stages + S::kRowsAt);
+  float* scales = reinterpret_cast<float*>(stages + S::kScalesAt);
   // log2(e) and the softmax scale; an 8-bit cache carries it in K's scales
   const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_BF16 ? c2 : 1.f;
 
@@ -376,7 +374,7 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   // --- the waves of the workgroup ---
   seen = __syncthreads_or(seen || bad);                      // a position without a page is seen too
   float* sums = reinterpret_cast<float*>(sa_smem);           // [wave][16 heads][D], then [wave][16] (m, l)
-  float2* stats = reinterpret_cast<float2*>(sums + S::kWaves * 16 * D);
+  float2* stats = reinterpret_cast<float2*>(sums + waves * 16 * D);
   bad = __syncthreads_or(bad);
 #pragma unroll 1
   for (int t = 0; t < GT; ++t) {
@@ -392,14 +390,12 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
     }
     __syncthreads();
     const int heads = min(16, group - 16 * t);
-    for (int x = tid; x < heads * (D / 4); x += S::kThreads) {
+    for (int x = tid; x < heads * (D / 4); x += 64 * waves) {
       const int h = x / (D / 4), d = x % (D / 4) * 4;
       float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < S::kWaves; ++i) top = fmaxf(top, stats[i * 16 + h].x);
+      for (int i = 0; i < waves; ++i) top = fmaxf(top, stats[i * 16 + h].x);
       float all = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < S::kWaves; ++i) {
+      for (int i = 0; i < waves; ++i) {
         const float2 ml = stats[i * 16 + h];
         const float keep = ml.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);   // without keys l and O are 0, or NaN
         const float4 v = *reinterpret_cast<const float4*>(sums + (i * 16 + h) * D + d);
@@ -464,12 +460,10 @@ hipError_t run(const SparseArgs& a, hipStream_t s) {
   using S = SparseShape<DT, D>;
   const int group = a.n_q_heads / a.c.n_kv_heads, tiles = (group + 16 * GT - 1) / (16 * GT);
   const int64_t items = a.c.n_rows * a.c.n_kv_heads * tiles;
-  // Workgroups to an item: as many as fill the chip twice, while each wave has
-  // two steps of its own.
   const int64_t keys = (int64_t)a.n_take * a.c.page_size + a.c.page_size + a.max_nodes;
-  const int64_t most = std::max<int64_t>(1, keys / (32 * S::kWaves * 2));
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMaxParts / items), (512 + items - 1) / items));
-  sparse_attention_kernel<DT, D, GT><<<(unsigned)(items * splits), S::kThreads, S::kLds, s>>>(a, group, tiles, splits);
+  const Spread x = spread<S>(items, GT, keys, kMaxParts);
+  const int splits = x.splits;
+  sparse_attention_kernel<DT, D, GT><<<(unsigned)(items * splits), 64 * x.waves, x.waves * S::kWaveLds, s>>>(a, group, tiles, splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const int pieces = (std::min(group, 16 * GT) * D + 1023) / 1024;

@@ -2,6 +2,8 @@
 // (sparse_attn.hip) and the rows of a request together (sparse_tile.hip).
 #pragma once
 
+#include <algorithm>
+
 #include "kv_mfma.h"
 #include "kv_sparse.h"
 
@@ -13,18 +15,23 @@ template <int DT, int D>
 struct SparseShape {
   static constexpr int kRB = D * (DT == DFLASH_BF16 ? 2 : 1);
   static constexpr int kChunks = kRB / 16;
-  static constexpr int kWaves = kRB == 512 ? 2 : 4, kThreads = 64 * kWaves;
+  static constexpr int kWaves = kRB == 512 ? 2 : 4, kThreads = 64 * kWaves;   // of a workgroup, at most
   static constexpr int kTile = 32 * kRB;                              // K (or V) of a step
   static constexpr int kLoads = kTile / 1024;                         // direct loads of K (or V) a lane
   static constexpr int kWaveStages = 2 * 2 * kTile;
-  static constexpr int kRowsAt = kWaves * kWaveStages;                // [wave][4 steps][32] byte offsets, int64
-  static constexpr int kScalesAt = kRowsAt + kWaves * 4 * 32 * 8;     // [wave][4 steps][K 32, V 32] fp32
-  static constexpr int kMasksAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : kWaves * 4 * 64 * 4);   // [wave][4 steps][32], of tiles
-  static constexpr int kLoop = kMasksAt + kWaves * 4 * 32 * 4;
-  static constexpr int kJoin = kWaves * 16 * (D + 2) * 4;             // after the loop: [wave] O, m and l of 16 rows
-  static constexpr int kLds = kLoop > kJoin ? kLoop : kJoin;
-  static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;            // workgroups that a CU holds
-  static_assert(kLds <= 160 * 1024 && 2 * kLoads < 63, "LDS of a CU, loads in flight");
+  // A wave's LDS: the stages, then
+  static constexpr int kRowsAt = kWaveStages;                         // [4 steps][32] byte offsets, int64
+  static constexpr int kScalesAt = kRowsAt + 4 * 32 * 8;              // [4 steps][K 32, V 32] fp32
+  static constexpr int kMasksAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 4 * 64 * 4);   // [4 steps][32], of tiles
+  static constexpr int kLoop = kMasksAt + 4 * 32 * 4;
+  static constexpr int kJoin = 16 * (D + 2) * 4;                      // after the loop: O, m and l of 16 rows
+  static constexpr int kWaveLds = kLoop > kJoin ? kLoop : kJoin;
+  static_assert(kWaves * kWaveLds <= 160 * 1024 && 2 * kLoads < 63, "LDS of a CU, loads in flight");
+  // Waves that a CU holds of a kernel with row_tiles * D sums to a lane group: by
+  // its LDS, and with more than 256 registers one to a SIMD.
+  static constexpr int cu_waves(int row_tiles) {
+    return kWaves * kWaveLds <= 80 * 1024 && row_tiles * D <= 128 ? 2 * kWaves : kWaves;
+  }
 
   // Chunk c of stage row r lies in slot c ^ swizzle(r), so that reads of one
   // instruction fall on different banks: for K, 16 consecutive rows of one
@@ -38,6 +45,26 @@ struct SparseShape {
     else return ((r / kRowsPerBanks) & (n - 1)) | (((r >> 4) & 1) * n);
   }
 };
+
+// How items are spread over the chip: waves of a workgroup, workgroups to an item.
+struct Spread {
+  int waves, splits;
+};
+// As many waves as run at once.  Few items are split over workgroups, while each
+// wave has two steps of its own; of many, a workgroup has fewer waves and an item
+// takes longer, rather than that the last ones wait for a place: one item's
+// look-ups then run beside the products of others.  (bf16, 8 kv heads of 128, always
+// 4 waves and this way: 128 rows over 16 pages of 16 50 and 30 us, 50 rows over 64
+// 63 and 40, 200 rows 189 and 174; 48 x 16 drafted rows 451 and 391.)
+template <class S>
+Spread spread(int64_t items, int row_tiles, int64_t keys, int64_t max_parts) {
+  const int64_t places = 256 * S::cu_waves(row_tiles);
+  Spread x{S::kWaves, 1};
+  while (x.waves > 1 && items * x.waves > places) x.waves /= 2;
+  if (x.waves == S::kWaves)
+    x.splits = (int)std::max<int64_t>(1, std::min({keys / (32 * S::kWaves * 2), max_parts / items, places / S::kWaves / items}));
+  return x;
+}
 
 // x of the lanes 16, 32 and 48 away, combined.
 __device__ __forceinline__ float quarter_max(float x) {

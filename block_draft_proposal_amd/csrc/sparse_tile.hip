@@ -20,8 +20,6 @@
 // Measured: 32 requests of 16 drafted rows, 128 pages of 16 a row, 8 kv heads of
 // 128, 4 query heads each, bf16: 111 us and 6.9 for the unions, which name 490 MB
 // of keys and values, 4.4 TB/s; row by row 460 us.
-#include <algorithm>
-
 #include "sparse_core.h"
 
 namespace dflash {
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   __shared__ uint32_t node_sets[2];                // nodes that see anything; that see a position without a page
   __shared__ uint64_t odd_rows;
   const KvView& c = a.c;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, g16 = lane >> 4, l32 = lane & 31, group = per_group.d;
   // tiles of one kv head are neighbours on one XCD
   const uint32_t w = xcd_contiguous(blockIdx.x, gridDim.x);
@@ -225,13 +223,13 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   // the line: the union's pages, the tail, the nodes
   const int32_t chosen_keys = t.over ? 0 : lists.counts[t.row0 * c.n_kv_heads + head] * c.page_size;
   const int32_t tail = t.start - t.full * c.page_size, rest = t.over ? 0 : tail + (mask ? t.n : t.n0 + t.nt);
-  const int64_t steps = ((int64_t)chosen_keys + rest + 31) / 32, slots = (int64_t)splits * S::kWaves, me = split * S::kWaves + wave;
+  const int64_t steps = ((int64_t)chosen_keys + rest + 31) / 32, slots = (int64_t)splits * waves, me = split * waves + wave;
   const int t0 = __builtin_amdgcn_readfirstlane((int)(steps * me / slots)), t1 = __builtin_amdgcn_readfirstlane((int)(steps * (me + 1) / slots));
 
-  unsigned char* stages = st_smem + wave * S::kWaveStages;
-  int64_t* row_at = reinterpret_cast<int64_t*>(st_smem + S::kRowsAt) + wave * 4 * 32;
-  float* scales = reinterpret_cast<float*>(st_smem + S::kScalesAt) + wave * 4 * 64;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(st_smem + S::kMasksAt) + wave * 4 * 32;
+  unsigned char* stages = st_smem + wave * S::kWaveLds;
+  int64_t* row_at = reinterpret_cast<int64_t*>(stages + S::kRowsAt);
+  float* scales = reinterpret_cast<float*>(stages + S::kScalesAt);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(stages + S::kMasksAt);
   const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_BF16 ? c2 : 1.f;
   if (tid == 0) {
     node_sets[0] = node_sets[1] = 0;
@@ -541,7 +539,7 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   if (seen) atomicOr(&node_sets[0], seen);
   if (bad) atomicOr(&node_sets[1], bad);
   float* sums = reinterpret_cast<float*>(st_smem);            // [wave][16 rows][D], then [wave][16] (m, l)
-  float2* stats = reinterpret_cast<float2*>(sums + S::kWaves * 16 * D);
+  float2* stats = reinterpret_cast<float2*>(sums + waves * 16 * D);
   float* part = lists.parts + (int64_t)w * part_floats(GT, D);
 #pragma unroll 1
   for (int u0 = 0; u0 < GT; ++u0) {
@@ -556,14 +554,12 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
         *reinterpret_cast<float4*>(sums + (wave * 16 + l16) * D + 16 * b + 4 * g16) = make_float4(o[u][b][0], o[u][b][1], o[u][b][2], o[u][b][3]);
     }
     __syncthreads();
-    for (int x = tid; x < min(16, rows - 16 * u0) * (D / 4); x += S::kThreads) {
+    for (int x = tid; x < min(16, rows - 16 * u0) * (D / 4); x += 64 * waves) {
       const int h = x / (D / 4), d = x % (D / 4) * 4, f_row = 16 * u0 + h;
       float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < S::kWaves; ++i) top = fmaxf(top, stats[i * 16 + h].x);
+      for (int i = 0; i < waves; ++i) top = fmaxf(top, stats[i * 16 + h].x);
       float all = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < S::kWaves; ++i) {
+      for (int i = 0; i < waves; ++i) {
         const float2 ml = stats[i * 16 + h];
         const float keep = ml.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);   // without keys l and O are 0
         const float4 v = *reinterpret_cast<const float4*>(sums + (i * 16 + h) * D + d);
@@ -606,7 +602,7 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
     __syncthreads();                               // the results are written, which a row alone replaces
     uint64_t odd = odd_rows;
     for (int i = 0; odd; odd &= odd - 1, ++i) {
-      if (i % S::kWaves != wave) continue;
+      if (i % waves != wave) continue;
       const int f_row = __builtin_ctzll(odd), my_node = per_group.div(f_row);
       if ((node_sets[0] >> my_node) & 1u) alone<DT, D>(a, t, my_node, head, head * group + (f_row - my_node * group));
     }
@@ -683,12 +679,10 @@ hipError_t run(const SparseArgs& a, const TilePlan& plan, hipStream_t s) {
   sparse_union_kernel<<<(unsigned)items, kUnionThreads, (size_t)c.table_width * 4, s>>>(a, lists, plan.nodes, plan.per_req);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // Workgroups to a tile: as many as run at once, while each wave has two steps
-  // of its own.
   const int64_t keys = (int64_t)a.n_take * c.page_size + c.page_size + a.max_nodes;
-  const int64_t most = std::max<int64_t>(1, keys / (32 * S::kWaves * 2));
-  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, kMaxTileParts / items), 256 * S::kPerCu / items));
-  sparse_tile_kernel<DT, D, GT><<<(unsigned)(items * splits), S::kThreads, S::kLds, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
+  const Spread x = spread<S>(items, GT, keys, kMaxTileParts);
+  const int splits = x.splits;
+  sparse_tile_kernel<DT, D, GT><<<(unsigned)(items * splits), 64 * x.waves, x.waves * S::kWaveLds, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
   if ((e = hipGetLastError()) != hipSuccess || splits == 1) return e;
   sparse_tile_join_kernel<DT, D, GT><<<(unsigned)(items * (16 * GT * D / 1024)), kThreads, 0, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
   return hipGetLastError();
