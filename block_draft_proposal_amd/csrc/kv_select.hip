@@ -45,8 +45,8 @@ __device__ __forceinline__ int32_t read_queries(const SelectArgs& a, int group, 
   constexpr int kWaves = T / 64, kMine = NT < kWaves ? 1 : NT / kWaves;   // rows of a wave
   const int pieces = group * kVecs;
   u32x4 held[kMine][2];
-  const auto row_of = [&](int i) { return min(wave + i * kWaves, NT - 1); };
-  const auto query_of = [&](int i) { return a.q + min(row0 + row_of(i), c.n_rows - 1) * a.q_row + (int64_t)head * group * a.q_head; };
+  const auto tile_row = [&](int i) { return min(wave + i * kWaves, NT - 1); };
+  const auto query_of = [&](int i) { return a.q + min(row0 + tile_row(i), c.n_rows - 1) * a.q_row + (int64_t)head * group * a.q_head; };
 #pragma unroll
   for (int i = 0; i < kMine; ++i)
 #pragma unroll
@@ -54,13 +54,12 @@ __device__ __forceinline__ int32_t read_queries(const SelectArgs& a, int group, 
       const int x = min(lane + 64 * j, pieces - 1);
       held[i][j] = ld16(query_of(i) + (int64_t)(x / kVecs) * a.q_head + (x % kVecs) * 8);
     }
-  int32_t req = 0;
-  int64_t pos = 0;
-  kv_row_position(c, row0, row0, req, pos);
+  RowOf at;
+  row_of(c, row0, a.max_nodes, at);
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     if (wave + i * kWaves >= NT) break;
-    const int n = row_of(i);
+    const int n = tile_row(i);
     const uint16_t* qp = query_of(i);
     uint32_t top = 0;
     auto widen = [&](u32x4 w) {
@@ -100,7 +99,7 @@ __device__ __forceinline__ int32_t read_queries(const SelectArgs& a, int group, 
     for (int x = pieces + lane; x < steps * kHeads * kVecs; x += 64) store(ld16(qp + (int64_t)(group - 1) * a.q_head + (x % kVecs) * 8), x);
   }
   __syncthreads();
-  return req;
+  return at.req;
 }
 
 // The keys of blocks first_block .. end_block - 1 of the tile's rows, 16 TT
@@ -280,10 +279,9 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
   uint32_t k[kOwn];
   load_keys<T, kOwn>(keys, tid, 0, c.table_width, k);
   const int64_t row = blockIdx.x / (unsigned)c.n_kv_heads;
-  int32_t req = 0;
-  int64_t pos = 0;
-  if (!kv_row_position(c, row, row, req, pos) || row - c.offsets[req] >= a.max_nodes) return;   // the same in every thread
-  const int32_t blocks = kv_blocks(c, c.start[req]), take = a.n_take;
+  RowOf at;
+  if (!row_of(c, row, a.max_nodes, at) || row - at.first >= a.max_nodes) return;   // the same in every thread
+  const int32_t blocks = kv_blocks(c, at.start), take = a.n_take;
   int32_t* out = a.out + (int64_t)blockIdx.x * take;
   if (blocks <= take) {
     for (int i = tid; i < take; i += T) out[i] = i < blocks ? i : -1;
@@ -594,10 +592,9 @@ __global__ void __launch_bounds__(kThreads) select_take_wave_kernel(SelectArgs a
 #pragma unroll
   for (int i = 0; i < KPL; ++i) k[i] = keys[min(i * 64 + lane, c.table_width - 1)];
   const int64_t row = item / c.n_kv_heads;
-  int32_t req = 0;
-  int64_t pos = 0;
-  if (!kv_row_position(c, row, row, req, pos) || row - c.offsets[req] >= a.max_nodes) return;   // the same in every lane
-  const int32_t blocks = __builtin_amdgcn_readfirstlane(kv_blocks(c, c.start[req])), take = a.n_take;
+  RowOf at;
+  if (!row_of(c, row, a.max_nodes, at) || row - at.first >= a.max_nodes) return;   // the same in every lane
+  const int32_t blocks = __builtin_amdgcn_readfirstlane(kv_blocks(c, at.start)), take = a.n_take;
   int32_t* out = a.out + item * take;
   if (blocks <= take) {
     for (int i = lane; i < take; i += 64) out[i] = i < blocks ? i : -1;

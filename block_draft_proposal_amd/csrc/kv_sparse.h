@@ -37,6 +37,30 @@ __device__ __forceinline__ int32_t kv_blocks(const KvView& c, int32_t start) {
   return start <= 0 ? 0 : min(c.per_page.div(start), c.table_width);
 }
 
+// A row's request, its first row and the one behind its last, its start.
+struct RowOf {
+  int32_t req, start;
+  int64_t first, end;
+};
+// false for padding.  Every lane of a wave has the same row.  Where all requests
+// before have max_nodes rows (single tokens, blocks of one size) the request is
+// known, and one round of loads has it all; else it is searched for.
+__device__ __forceinline__ bool row_of(const KvView& c, int64_t row, int32_t max_nodes, RowOf& r) {
+  r.req = (int32_t)min((uint32_t)row / (uint32_t)max_nodes, (uint32_t)c.n_req - 1u);
+  r.first = c.offsets[r.req];
+  r.end = c.offsets[r.req + 1];
+  r.start = c.start[r.req];
+  if (row < r.first || row >= r.end || row >= c.n_rows) {
+    int64_t pos = 0;
+    if (!kv_row_position(c, row, row, r.req, pos)) return false;
+    r.first = c.offsets[r.req];
+    r.end = c.offsets[r.req + 1];
+    r.start = c.start[r.req];
+  }
+  r.req = __builtin_amdgcn_readfirstlane(r.req);
+  return true;
+}
+
 hipError_t launch_kv_bounds(const KvView& c, int8_t* codes, uint8_t* scale, const int32_t* end, hipStream_t stream);
 size_t kv_select_bytes(int64_t n_rows, int32_t n_kv_heads, int32_t table_width);
 hipError_t launch_kv_select(const SelectArgs& a, hipStream_t stream);

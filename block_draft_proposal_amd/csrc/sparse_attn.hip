@@ -67,24 +67,30 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   const Item it = item_of(w / (uint32_t)splits, (uint32_t)c.n_rows, tiles);
   const int head = it.head, h0 = it.tile * 16 * GT, group = min(all_heads - h0, 16 * GT);   // its query heads
   const int64_t row = it.row;
-  int32_t req = 0;
-  int64_t at_pos = 0;
-  if (!kv_row_position(c, row, row, req, at_pos)) return;   // padding: the whole workgroup
-  req = __builtin_amdgcn_readfirstlane(req);
-  const int64_t first = c.offsets[req];
-  const int node = (int)(row - first);
+  const int32_t* chosen = a.blocks + ((int64_t)row * c.n_kv_heads + head) * a.n_take;
+  int32_t named[4];                                // the first 256 entries, while the request is looked up
+  if (a.n_take > 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) named[i] = chosen[min(lane + 64 * i, a.n_take - 1)];
+  }
+  RowOf at;
+  if (!row_of(c, row, a.max_nodes, at)) return;     // padding: the whole workgroup
+  const int32_t req = at.req;
+  const int node = (int)(row - at.first);
   if (node >= a.max_nodes) return;
-  const int n = (int)min(min((int64_t)c.offsets[req + 1], c.n_rows) - first, (int64_t)a.max_nodes);
-  const int32_t start = max(c.start[req], 0);
+  const int n = (int)min(min(at.end, c.n_rows) - at.first, (int64_t)a.max_nodes);
+  const int32_t start = max(at.start, 0);
   const bool over = (int64_t)start + n > min((int64_t)kMaxLen, (int64_t)c.table_width * c.page_size);
   const int32_t full = kv_blocks(c, start);                 // blocks that may be chosen
   const int32_t* table = c.table + req * c.table_stride;
-  const int32_t* chosen = a.blocks + ((int64_t)row * c.n_kv_heads + head) * a.n_take;
   const uint32_t* mask = a.mask ? reinterpret_cast<const uint32_t*>(a.mask + (int64_t)row * a.mask_words) : nullptr;
 
   // the line: entries up to the last that names a block, the tail, the nodes
   int used = 0;
-  for (int i = lane; i < a.n_take; i += 64) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 64 * i < a.n_take && named[i] >= 0 && named[i] < full) used = lane + 64 * i + 1;
+  for (int i = 256 + lane; i < a.n_take; i += 64) {
     const int32_t b = chosen[i];
     if (b >= 0 && b < full) used = i + 1;
   }
@@ -427,9 +433,8 @@ __global__ void __launch_bounds__(256) sparse_join_kernel(SparseArgs a, int all_
   const uint32_t item = blockIdx.x / (uint32_t)pieces;
   const Item it = item_of(item, (uint32_t)c.n_rows, tiles);
   const int h0 = it.tile * 16 * GT, group = min(all_heads - h0, 16 * GT);
-  int32_t req = 0;
-  int64_t pos = 0;
-  if (!kv_row_position(c, it.row, it.row, req, pos) || it.row - c.offsets[req] >= a.max_nodes) return;
+  RowOf at;
+  if (!row_of(c, it.row, a.max_nodes, at) || it.row - at.first >= a.max_nodes) return;
   const int x = ((int)(blockIdx.x - item * (uint32_t)pieces) * 256 + (int)threadIdx.x) * 4, h = x / D, d = x % D;
   if (h >= group) return;
   const int64_t size = Part::floats(min(all_heads, 16 * GT), D);

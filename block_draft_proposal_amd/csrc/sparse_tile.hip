@@ -67,12 +67,12 @@ __device__ __forceinline__ bool tile_at(const SparseArgs& a, int tile, int nodes
   const KvView& c = a.c;
   t.req = tile / per_req;
   t.n0 = (tile - t.req * per_req) * nodes;
-  const int64_t first = c.offsets[t.req];
-  t.n = (int)max((int64_t)0, min(min((int64_t)c.offsets[t.req + 1], c.n_rows) - first, (int64_t)a.max_nodes));
+  const int64_t first = c.offsets[t.req], end = c.offsets[t.req + 1];
+  t.start = max(c.start[t.req], 0);               // with the offsets, not behind them
+  t.n = (int)max((int64_t)0, min(min(end, c.n_rows) - first, (int64_t)a.max_nodes));
   t.nt = min(nodes, t.n - t.n0);
   if (first < 0 || t.nt <= 0) return false;
   t.row0 = first + t.n0;
-  t.start = max(c.start[t.req], 0);
   t.full = kv_blocks(c, t.start);
   t.over = (int64_t)t.start + t.n > min((int64_t)kMaxLen, (int64_t)c.table_width * c.page_size);
   return true;
@@ -679,7 +679,10 @@ hipError_t run(const SparseArgs& a, const TilePlan& plan, hipStream_t s) {
   sparse_union_kernel<<<(unsigned)items, kUnionThreads, (size_t)c.table_width * 4, s>>>(a, lists, plan.nodes, plan.per_req);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t keys = (int64_t)a.n_take * c.page_size + c.page_size + a.max_nodes;
+  // Keys of a tile: the union is as long as its nodes' pages differ, taken for
+  // twice a node's.  (One request of 16 nodes, 64 pages each out of 128: by one
+  // node's pages 37 us, twice 35, four times 36; out of 1024 pages 77, 58, 49.)
+  const int64_t keys = (int64_t)a.n_take * std::min(plan.nodes, 2) * c.page_size + c.page_size + a.max_nodes;
   const Spread x = spread<S>(items, GT, keys, kMaxTileParts);
   const int splits = x.splits;
   sparse_tile_kernel<DT, D, GT><<<(unsigned)(items * splits), 64 * x.waves, x.waves * S::kWaveLds, s>>>(a, lists, per_group, plan.nodes, plan.per_req, splits);
