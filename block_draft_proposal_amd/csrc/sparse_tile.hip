@@ -557,17 +557,21 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
     for (int x = tid; x < min(16, rows - 16 * u0) * (D / 4); x += 64 * waves) {
       const int h = x / (D / 4), d = x % (D / 4) * 4, f_row = 16 * u0 + h;
       float top = -INFINITY;
-      for (int i = 0; i < waves; ++i) top = fmaxf(top, stats[i * 16 + h].x);
+      // (as many reads as waves at most, so that they go out at once)
+#pragma unroll
+      for (int i = 0; i < S::kWaves; ++i) top = fmaxf(top, stats[min(i, waves - 1) * 16 + h].x);
       float all = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int i = 0; i < waves; ++i) {
-        const float2 ml = stats[i * 16 + h];
+#pragma unroll
+      for (int i = 0; i < S::kWaves; ++i) {
+        const int w1 = min(i, waves - 1);
+        const float2 ml = stats[w1 * 16 + h];
         const float keep = ml.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);   // without keys l and O are 0
-        const float4 v = *reinterpret_cast<const float4*>(sums + (i * 16 + h) * D + d);
-        all += ml.y * keep;
-        f[0] += v.x * keep;
-        f[1] += v.y * keep;
-        f[2] += v.z * keep;
-        f[3] += v.w * keep;
+        const float4 v = *reinterpret_cast<const float4*>(sums + (w1 * 16 + h) * D + d);
+        all += i < waves ? ml.y * keep : 0.f;
+        f[0] += i < waves ? v.x * keep : 0.f;
+        f[1] += i < waves ? v.y * keep : 0.f;
+        f[2] += i < waves ? v.z * keep : 0.f;
+        f[3] += i < waves ? v.w * keep : 0.f;
       }
       if (splits == 1) {
         const int my_node = per_group.div(f_row);
