@@ -23,8 +23,8 @@
 // partial sums in a fixed order.
 //
 // Measured: 128 single rows over 64 pages of 32 each, 8 kv heads of 128, 64 query
-// heads, e4m3 (541 MB): 110 us, 4.9 TB/s, what a copy of 2 GB reaches on the same
-// card.  One row over 32 pages of 64, bf16 (8.4 MB): 10.8 us and 2.7 for the
+// heads, e4m3 (541 MB): 103 us, 5.2 TB/s, more than a copy of 2 GB reaches on the
+// same card.  One row over 32 pages of 64, bf16 (8.4 MB): 10.8 us and 2.7 for the
 // join: look-ups, loads and products of a dozen steps one after the other.
 #include "sparse_core.h"
 
@@ -100,9 +100,10 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   const int64_t steps = ((int64_t)chosen_keys + rest + 31) / 32, slots = (int64_t)splits * waves, me = split * waves + wave;
   const int t0 = __builtin_amdgcn_readfirstlane((int)(steps * me / slots)), t1 = __builtin_amdgcn_readfirstlane((int)(steps * (me + 1) / slots));
 
-  unsigned char* stages = sa_smem + wave * S::kWaveLds;
-  int64_t* row_at = reinterpret_cast<int64_t*>(stages + S::kRowsAt);
-  float* scales = reinterpret_cast<float*>(stages + S::kScalesAt);
+  unsigned char* stages = sa_smem + wave * S::kWaveStages;
+  unsigned char* ring = sa_smem + waves * S::kWaveStages + wave * S::kRing;
+  int64_t* row_at = reinterpret_cast<int64_t*>(ring + S::kRowsAt);
+  float* scales = reinterpret_cast<float*>(ring + S::kScalesAt);
   // log2(e) and the softmax scale; an 8-bit cache carries it in K's scales
   const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_BF16 ? c2 : 1.f;
 
@@ -405,10 +406,10 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
       float all = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < S::kWaves; ++i) {
-        const int w1 = min(i, waves - 1);
-        const float2 ml = stats[w1 * 16 + h];
+        const int j = min(i, waves - 1);
+        const float2 ml = stats[j * 16 + h];
         const float keep = ml.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);   // without keys l and O are 0, or NaN
-        const float4 v = *reinterpret_cast<const float4*>(sums + (w1 * 16 + h) * D + d);
+        const float4 v = *reinterpret_cast<const float4*>(sums + (j * 16 + h) * D + d);
         all += i < waves ? ml.y * keep : 0.f;
         f[0] += i < waves ? v.x * keep : 0.f;
         f[1] += i < waves ? v.y * keep : 0.f;

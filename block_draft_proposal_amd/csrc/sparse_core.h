@@ -19,13 +19,13 @@ struct SparseShape {
   static constexpr int kTile = 32 * kRB;                              // K (or V) of a step
   static constexpr int kLoads = kTile / 1024;                         // direct loads of K (or V) a lane
   static constexpr int kWaveStages = 2 * 2 * kTile;
-  // A wave's LDS: the stages, then
-  static constexpr int kRowsAt = kWaveStages;                         // [4 steps][32] byte offsets, int64
-  static constexpr int kScalesAt = kRowsAt + 4 * 32 * 8;              // [4 steps][K 32, V 32] fp32
+  // LDS: the waves' stages, then a ring of each
+  static constexpr int kRowsAt = 0;                                   // [4 steps][32] byte offsets, int64
+  static constexpr int kScalesAt = 4 * 32 * 8;                        // [4 steps][K 32, V 32] fp32
   static constexpr int kMasksAt = kScalesAt + (DT == DFLASH_BF16 ? 0 : 4 * 64 * 4);   // [4 steps][32], of tiles
-  static constexpr int kLoop = kMasksAt + 4 * 32 * 4;
+  static constexpr int kRing = kMasksAt + 4 * 32 * 4;
   static constexpr int kJoin = 16 * (D + 2) * 4;                      // after the loop: O, m and l of 16 rows
-  static constexpr int kWaveLds = kLoop > kJoin ? kLoop : kJoin;
+  static constexpr int kWaveLds = kWaveStages + kRing > kJoin ? kWaveStages + kRing : kJoin;
   static_assert(kWaves * kWaveLds <= 160 * 1024 && 2 * kLoads < 63, "LDS of a CU, loads in flight");
   // Waves that a CU holds of a kernel with row_tiles * D sums to a lane group: by
   // its LDS, and with more than 256 registers one to a SIMD.

@@ -18,8 +18,8 @@
 // over its own keys alone.
 //
 // Measured: 32 requests of 16 drafted rows, 128 pages of 16 a row, 8 kv heads of
-// 128, 4 query heads each, bf16: 111 us and 6.9 for the unions, which name 490 MB
-// of keys and values, 4.4 TB/s; row by row 460 us.
+// 128, 4 query heads each, bf16: 109 to 116 us and 7 for the unions, which name 490
+// MB of keys and values, 4.0 to 4.3 TB/s; row by row 460 us.
 #include "sparse_core.h"
 
 namespace dflash {
@@ -226,10 +226,11 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
   const int64_t steps = ((int64_t)chosen_keys + rest + 31) / 32, slots = (int64_t)splits * waves, me = split * waves + wave;
   const int t0 = __builtin_amdgcn_readfirstlane((int)(steps * me / slots)), t1 = __builtin_amdgcn_readfirstlane((int)(steps * (me + 1) / slots));
 
-  unsigned char* stages = st_smem + wave * S::kWaveLds;
-  int64_t* row_at = reinterpret_cast<int64_t*>(stages + S::kRowsAt);
-  float* scales = reinterpret_cast<float*>(stages + S::kScalesAt);
-  uint32_t* masks = reinterpret_cast<uint32_t*>(stages + S::kMasksAt);
+  unsigned char* stages = st_smem + wave * S::kWaveStages;
+  unsigned char* ring = st_smem + waves * S::kWaveStages + wave * S::kRing;
+  int64_t* row_at = reinterpret_cast<int64_t*>(ring + S::kRowsAt);
+  float* scales = reinterpret_cast<float*>(ring + S::kScalesAt);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(ring + S::kMasksAt);
   const float c2 = a.scale * 1.44269504088896340736f, cs = DT == DFLASH_BF16 ? c2 : 1.f;
   if (tid == 0) {
     node_sets[0] = node_sets[1] = 0;
@@ -563,10 +564,10 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
       float all = 0.f, f[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < S::kWaves; ++i) {
-        const int w1 = min(i, waves - 1);
-        const float2 ml = stats[w1 * 16 + h];
+        const int j = min(i, waves - 1);
+        const float2 ml = stats[j * 16 + h];
         const float keep = ml.x == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);   // without keys l and O are 0
-        const float4 v = *reinterpret_cast<const float4*>(sums + (w1 * 16 + h) * D + d);
+        const float4 v = *reinterpret_cast<const float4*>(sums + (j * 16 + h) * D + d);
         all += i < waves ? ml.y * keep : 0.f;
         f[0] += i < waves ? v.x * keep : 0.f;
         f[1] += i < waves ? v.y * keep : 0.f;
