@@ -153,3 +153,36 @@ def test_two_streams_with_workspaces_of_their_own(nodes):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+@pytest.mark.parametrize("n,nodes,heads", [(20, 16, 8), (2, 5, 2), (40, 1, 8)])
+def test_a_captured_choice_and_attention(n, nodes, heads):
+    """Enough tiles for one launch of the choice, few tiles that are split, and
+    single rows: replays over new queries, with eager calls and waits between."""
+    require_gpu()
+    say(f"captured {n} {nodes}")
+    page, dim, length = 16, 128, 1000
+    width = -(-(length + nodes) // page)
+    cache = D.KVCache.empty(n * width, heads, page, dim, torch.bfloat16)
+    table = torch.randperm(n * width, generator=torch.Generator().manual_seed(2)).view(n, width).int().to(DEV)
+    k = rand_rows((length + nodes) * n, heads, dim, "bf16", 1)
+    D.dflash_kv_write(cache, k, k, page_table=table, start=gpu(np.zeros(n)), offsets=gpu(np.arange(n + 1) * (length + nodes)))
+    b, start = D.KVBounds.empty(cache), gpu(length - 7 * np.arange(n))
+    D.dflash_kv_bounds(cache, b, page_table=table, start=gpu(np.zeros(n)), end=start)
+    batch = dict(page_table=table, start=start, offsets=gpu(np.arange(n + 1) * nodes), max_nodes=nodes)
+    q = rand_rows(n * nodes, heads * 4, dim, "bf16", 5)
+
+    def ask():
+        blocks = D.dflash_kv_select(q, b, n_take=12, **batch)
+        return blocks, D.dflash_sparse_attention(q, cache, blocks, **batch)
+
+    ask()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ask()
+    for seed in range(4):
+        q.copy_(rand_rows(n * nodes, heads * 4, dim, "bf16", 10 + seed))
+        want = ask()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), seed

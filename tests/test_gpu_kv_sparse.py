@@ -367,6 +367,18 @@ def test_sparse_splits(kind, n_req, rows):
     check_sparse(cache, tensors, plan, host, n_rows, 3, blocks)
 
 
+@pytest.mark.parametrize("kind,dim,heads,n_req,rows", [
+    ("bf16", 128, 16, 18, 1), ("bf16", 128, 16, 40, 1), ("bf16", 128, 16, 80, 1), ("i8", 64, 16, 50, 1), ("e4m3", 128, 32, 70, 1), ("bf16", 256, 16, 20, 1),
+    ("bf16", 256, 16, 40, 1), ("i8", 256, 16, 20, 1), ("bf16", 128, 16, 20, 2), ("e4m3", 64, 32, 40, 3), ("i8", 128, 16, 70, 2), ("bf16", 256, 16, 33, 2)])
+def test_sparse_of_fewer_waves_to_a_workgroup(kind, dim, heads, n_req, rows):
+    """More items than workgroups run at once: four, two and one wave to each."""
+    require_gpu()
+    say(f"waves {kind} {dim} {heads} {n_req} {rows}")
+    start = [170 - 7 * r % 150 for r in range(n_req)]
+    cache, tensors, plan, host, n_rows = written(kind, start, [rows] * n_req, 16, heads, dim)
+    check_sparse(cache, tensors, plan, host, n_rows, 2, pick(host, n_rows, heads, 16, 6, 2))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
 def test_all_blocks_are_the_whole_prefix(kind):
     """With every block chosen, it is the tree attention over the prefix."""
