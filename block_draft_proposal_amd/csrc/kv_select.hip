@@ -660,7 +660,7 @@ hipError_t run(const SelectArgs& a, hipStream_t s) {
     }
   }
   // Blocks of a workgroup: a share that makes as many workgroups as run at once.
-  constexpr int kStep = 64 * kThreads / 64;
+  constexpr int kStep = 16 * 4 * (kThreads / 64);   // of its step
   const int64_t wanted = std::max<int64_t>(1, 768 / tiles);
   const int64_t share = (a.c.table_width + wanted - 1) / wanted;
   const int64_t chunk = (share + kStep - 1) / kStep * kStep;
