@@ -129,7 +129,7 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) o[t][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  bool bad = over, seen = over;
+  bool bad = over && sees_any(a, row, head, full, tail, n), seen = bad;
 
   // Two values to choose from, not two places of the arguments to load one from.
   uint64_t k_scales = reinterpret_cast<uint64_t>(c.k_scale), v_scales = reinterpret_cast<uint64_t>(c.v_scale);

@@ -88,6 +88,20 @@ __device__ __forceinline__ void in_accumulators(f32x4_t& x) {
   if constexpr (MANY) asm volatile("" : "+a"(x));
 }
 
+// Whether a row sees anything: a block that its list names, the tail or a node.
+// The kernels find that as they walk the row's keys; this is for requests whose
+// length is beyond the table, which have none.  All lanes of a wave ask together.
+__device__ __forceinline__ bool sees_any(const SparseArgs& a, int64_t row, int head, int32_t full, int32_t tail, int n) {
+  if (tail > 0 || !a.mask) return true;            // a chain: every node sees itself
+  const int lane = threadIdx.x & 63;
+  const int32_t* chosen = a.blocks + (row * a.c.n_kv_heads + head) * a.n_take;
+  const uint64_t* mask = a.mask + row * a.mask_words;
+  bool any = false;
+  for (int i = lane; i < a.n_take; i += 64) any = any || (chosen[i] >= 0 && chosen[i] < full && (i == 0 || chosen[i] > chosen[i - 1]));
+  for (int w = lane; 64 * w < n; w += 64) any = any || (mask[w] & (n - 64 * w >= 64 ? ~0ull : (1ull << (n - 64 * w)) - 1));
+  return __any(any);
+}
+
 // Whether rows of a request attend together, and how.
 struct TilePlan {
   bool use;

@@ -261,7 +261,11 @@ __global__ void __launch_bounds__((SparseShape<DT, D>::kThreads), (GT * D <= 128
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) o[u][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  uint32_t seen = t.over ? all_nodes : 0, bad = seen;   // over this lane's keys
+  uint32_t seen = 0, bad = 0;                      // over this lane's keys
+  if (t.over) {
+    for (int i = 0; i < t.nt; ++i) seen |= (uint32_t)sees_any(a, t.row0 + i, head, t.full, tail, t.n) << i;
+    bad = seen;
+  }
 
   // Two values to choose from, not two places of the arguments to load one from.
   uint64_t k_scales = reinterpret_cast<uint64_t>(c.k_scale), v_scales = reinterpret_cast<uint64_t>(c.v_scale);

@@ -99,7 +99,8 @@ int dflash_kv_select(const dflash_page_bounds* bounds, const dflash_kv_batch* ba
  * A row that sees nothing gets zeros.  What a row does not see has no effect on
  * it, whatever values the cache holds there, but for the last bits: the nodes of
  * a request are taken together.  Positions without a page in the pool make the
- * rows that see them NaN; so do lengths beyond the table.
+ * rows that see them NaN; a length (start plus nodes) beyond the table makes all
+ * rows of its request NaN that see anything.
  * Arithmetic: as for dflash_tree_attention; an infinity or a NaN among the
  * values that a row sees makes its result an infinity or a NaN.  A call's
  * result is the same every time; its sums are split by the whole batch, so a
