@@ -168,7 +168,7 @@ def _call(fn, cache: KVCache, stream, *args) -> None:
         raise ValueError("stream belongs to another GPU than the cache")
     else:
         handle = stream.cuda_stream
-    if index == torch._C._cuda_getDevice():
+    if index == torch.cuda.current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
