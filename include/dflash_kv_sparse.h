@@ -101,10 +101,13 @@ int dflash_kv_select(const dflash_page_bounds* bounds, const dflash_kv_batch* ba
  * a request are taken together.  Positions without a page in the pool make the
  * rows that see them NaN; a length (start plus nodes) beyond the table makes all
  * rows of its request NaN that see anything.
- * Arithmetic: as for dflash_tree_attention; an infinity or a NaN among the
- * values that a row sees makes its result an infinity or a NaN.  A call's
- * result is the same every time; its sums are split by the whole batch, so a
- * request may differ in the last bits from one batch to another.
+ * Arithmetic: as for dflash_tree_attention.  A NaN among the keys that a row sees
+ * makes its result NaN; an infinity or a NaN among the values makes it an
+ * infinity or a NaN in that channel.  A key with an infinity has the score that
+ * the product gives it: at -infinity its weight is 0 (a row whose keys all have
+ * that is NaN), at +infinity the row is NaN.  A call's result is the same every
+ * time; its sums are split by the whole batch, so a request may differ in the
+ * last bits from one batch to another.
  *   max_nodes also decides whether the nodes of a request are taken together:
  *           give the batch's own largest number, 1 for plain decoding.
  * n_rows * n_kv_heads is at most 2^21, n_take * page_size at most 2^30.
