@@ -267,7 +267,7 @@ __device__ __forceinline__ float key_score(uint32_t key) { return __uint_as_floa
 // (one row of 8192 blocks, 8 heads: 11 bits of the key at a time 29 us, so 10).
 template <int T, int kOwn>
 __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
-  constexpr int kSegment = kOwn * T, kBins = 8 * T < 2048 ? 8 * T : 2048, kEach = kBins / T, kFew = 64;
+  constexpr int kSegment = kOwn * T, kBins = 2048, kEach = kBins / T, kFew = 64;
   __shared__ uint32_t bins[kBins];
   __shared__ uint32_t sums[2][T / 64], lows[T / 64], highs[T / 64];
   __shared__ uint32_t few[kFew];
@@ -316,7 +316,6 @@ __global__ void __launch_bounds__(T) select_take_kernel(SelectArgs a) {
     lows[wave] = low;
     highs[wave] = high;
   }
-  // 2^24 blocks at most over at least 256 threads: both counts fit a word of 64 bits' halves in turn
   forced = all_waves<T>(wave_sum_u32(forced), sums, at_sum);
   broken = all_waves<T>(wave_sum_u32(broken), sums, at_sum);
 #pragma unroll
