@@ -1,5 +1,6 @@
-"""Runs cases of perf/operators.py through the framework's calls: by the clock,
-or under a profiler whose files it then sums up.
+"""Runs cases of perf/operators.py, or with --more of perf/more_operators.py,
+through the framework's calls: by the clock, or under a profiler whose files it
+then sums up.
 
     python3 perf/profile_operators.py clock            us a pass, passes captured into one graph
     python3 perf/profile_operators.py run              the passes alone, for a profiler
@@ -7,9 +8,10 @@ or under a profiler whose files it then sums up.
 
 Each takes the same selection, and `table` the one of its `run`: --only NAME,NAME
 for listed cases (all by default), any number of --case KEY=VALUE,... for others
-(those alone, without --only).  A --case starts from a bf16 chain of 32 query and
-8 kv heads of 128 on pages of 16; even=1 gives every request the same lengths.
-Three sets of inputs are taken in turn."""
+of perf/operators.py (those alone, without --only).  A --case starts from a bf16
+chain of 32 query and 8 kv heads of 128 on pages of 16; even=1 gives every
+request the same lengths.  With --more a pass is any number of launches, and a
+profile is of one case.  Three sets of inputs are taken in turn."""
 import argparse
 import csv
 import glob
@@ -22,8 +24,10 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import numpy as np
 import torch
 
-import perf.operators as M
+import perf.more_operators
+import perf.operators
 
+M = perf.operators
 DEFAULT = dict(op="tree", n_req=1, hq=32, hkv=8, dim=128, page=16, type="bf16", io="bf16", mask="chain")
 RAGGED = M._plan
 
@@ -86,11 +90,18 @@ def _dispatches(folder, pattern):
 
 
 def _kernel(name):
-    return re.sub(r".*::(\w+)<([^>]*)>.*", r"`\1<\2>`", name)
+    return "`" + re.search(r"\w+_kernel(<[^>]*>)?", name)[0] + "`"
 
 
 def _by_case(args, dispatches):
-    """(case, kernel, its dispatches): a pass of the attention is two of them."""
+    """(case, kernel, its dispatches), without those of the first passes: a pass
+    of the tree attention is two of them, one of its file's other operators one."""
+    if args.more:
+        case, = selected(args)
+        for kernel in dict.fromkeys(_kernel(d[0]["Kernel_Name"]) for d in dispatches):
+            mine = [d for d in dispatches if _kernel(d[0]["Kernel_Name"]) == kernel]
+            yield case, kernel, mine[len(mine) * 3 // (args.passes + 3):]
+        return
     at = 0
     for case in selected(args):
         n = (args.passes + 3) * (2 if case["op"] == "tree" else 1)
@@ -105,8 +116,9 @@ def table(args):
     for case, kernel, mine in _by_case(args, [[r] for r in trace]) if trace else ():
         r = mine[0][0]
         us = sorted((int(d[0]["End_Timestamp"]) - int(d[0]["Start_Timestamp"])) / 1e3 for d in mine)
-        shape = " | ".join(r[x] for x in ("Grid_Size_X", "Workgroup_Size_X", "VGPR_Count", "Accum_VGPR_Count", "LDS_Block_Size"))
-        print(f"| {case['name']} | {kernel} | {shape} | {len(us)} | {us[0]:.1f} | {us[len(us) // 2]:.1f} | {us[-1]:.1f} |")
+        # the trace counts a wave's registers in pairs here, vector and accumulation together
+        shape = [r["Grid_Size_X"], r["Workgroup_Size_X"], 2 * (int(r["VGPR_Count"]) + int(r["Accum_VGPR_Count"])), r["LDS_Block_Size"]]
+        print(f"| {case['name']} | {kernel} | {' | '.join(map(str, shape))} | {len(us)} | {us[0]:.1f} | {us[len(us) // 2]:.1f} | {us[-1]:.1f} |")
     groups = {}
     for r in _dispatches(args.folder, "*counter_collection.csv"):
         groups.setdefault(int(r["Dispatch_Id"]), []).append(r)
@@ -124,9 +136,17 @@ def main():
     p.add_argument("folder", nargs="?")
     p.add_argument("--only")
     p.add_argument("--case", action="append", default=[])
+    p.add_argument("--more", action="store_true")
     p.add_argument("--passes", type=int, default=30)
     args = p.parse_args()
-    M.own, M._plan = True, _plan
+    if args.more and args.case:
+        p.error("--case is of perf/operators.py")
+    global M
+    if args.more:
+        M = perf.more_operators
+    else:
+        M._plan = _plan
+    M.own = True
     {"clock": clock, "run": run, "table": table}[args.what](args)
 
 
