@@ -9,10 +9,10 @@
 // to all of the next.  Where one workgroup holds pool and tables, a call is one.
 //
 // Planning moves little and is bound by latency: its floor is the launches.
-// Measured: 512 requests in a pool of half a million pages, a resize 17 us (let go
-// 5.0, count 2.6, plan 4.1, give 6.1), a fork 10, a compact's planning 22 (128
+// Measured: 512 requests in a pool of half a million pages, a resize 18 us (let go
+// 4.9, count 2.7, plan 4.2, give 6.5), a fork 10, a compact's planning 23 (128
 // requests, 32768 pages); 32 requests in a small pool 4 to 6 us a call.  Copies of
-// pages stream: 0.53 GB, read and written in 190 us, 5.6 TB/s.
+// pages stream: 0.53 GB, read and written in 192 us, 5.6 TB/s.
 #include <algorithm>
 
 #include "kv_pages.h"

@@ -11,10 +11,10 @@
 // What it cannot do without is one pass over the bounds, 256 bytes for a block
 // and kv head of 128 channels.  Blocks of 16 drafted rows do both in one
 // workgroup, their keys in LDS (32 requests x 16 rows, 8 kv heads, up to 2048
-// blocks, 100 MB of bounds: 40 to 45 us, the score 27 of them, 3.7 TB/s of bounds
+// blocks, 100 MB of bounds: 46 us, the score 27 of them, 3.7 TB/s of bounds
 // while it lasts).  Single rows, and few of them, are split over the chip with their
 // keys in the workspace, and a second launch chooses (one row of 8192 blocks, 8
-// heads: 11 + 10 us; a chain of small steps, and latency).
+// heads: 12 + 10 us; a chain of small steps, and latency).
 #include <algorithm>
 
 #include "kv_sparse.h"

@@ -23,9 +23,10 @@
 // partial sums in a fixed order.
 //
 // Measured: 128 single rows over 64 pages of 32 each, 8 kv heads of 128, 64 query
-// heads, e4m3 (541 MB): 103 us, 5.2 TB/s, more than a copy of 2 GB reaches on the
-// same card.  One row over 32 pages of 64, bf16 (8.4 MB): 10.8 us and 2.7 for the
-// join: look-ups, loads and products of a dozen steps one after the other.
+// heads, e4m3 (541 MB): 103 to 105 us, 5.2 TB/s, more than a copy of 2 GB reaches
+// on the same card.  One row over 32 pages of 64, bf16 (8.4 MB): 11.8 us and 3.9 for
+// the join.  Its 65 steps are two to a wave, and the way to them is what takes the
+// time: lengths and list, then four rounds of look-ups that each wait for the last.
 #include "sparse_core.h"
 
 namespace dflash {
